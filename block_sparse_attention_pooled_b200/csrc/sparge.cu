@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "sparge.h"
@@ -21,6 +22,9 @@
 #include "attn_bwd.cuh"
 #include "lin_bwd.cuh"
 #include "selftest.cuh"
+#include "window.cuh"
+#include "cache.cuh"
+#include "cache_attn.cuh"
 
 namespace {
 
@@ -931,3 +935,5 @@ const char* sparge_status_string(sparge_status status) {
 }
 
 }  // extern "C"
+
+#include "window_host.cuh"

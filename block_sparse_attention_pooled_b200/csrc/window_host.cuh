@@ -1,0 +1,233 @@
+// Host side of the windowed-attention and paged-cache entry points (included
+// by sparge.cu, which holds the shared checks and descriptor helpers).
+#pragma once
+
+namespace {
+
+struct WDims {
+  int64_t BH, BHkv, rows, keys;
+};
+
+bool window_ok(const sparge_window* w) {
+  return w != nullptr && w->left >= -1 && w->right >= -1 && w->sinks >= 0 && w->unit >= 1;
+}
+
+Window device_window(const sparge_window* w) { return Window{w->left, w->right, w->sinks, w->unit}; }
+
+sparge_status check_window(const sparge_window_shape* s, const sparge_window* w, WDims* out) {
+  if (s == nullptr || !window_ok(w)) return SPARGE_ERR_INVALID_ARG;
+  if (s->B <= 0 || s->H <= 0 || s->Hkv <= 0 || s->N <= 0 || s->d <= 0 || s->H % s->Hkv) return SPARGE_ERR_INVALID_ARG;
+  if (s->d != 64 && s->d != 128) return SPARGE_ERR_UNSUPPORTED;
+  out->BH = (int64_t)s->B * s->H;
+  out->BHkv = (int64_t)s->B * s->Hkv;
+  if (out->BHkv > 65535 || out->BH > INT32_MAX / 8) return SPARGE_ERR_UNSUPPORTED;
+  out->rows = out->BH * s->N;
+  out->keys = out->BHkv * s->N;
+  if (ceil_div(out->rows, 4) > INT32_MAX || s->N > (1 << 30)) return SPARGE_ERR_UNSUPPORTED;
+  return SPARGE_OK;
+}
+
+bool all_aligned16(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (p == nullptr || !aligned16(p)) return false;
+  return true;
+}
+
+size_t window_ws(int op, const WDims& d) {
+  return op == SPARGE_OP_WINDOW_BWD ? align256((size_t)d.rows * 4) : 0;
+}
+
+sparge_status check_ws(const void* ws, size_t have, size_t need) {
+  if (need == 0) return SPARGE_OK;
+  if (ws == nullptr || have < need || (reinterpret_cast<uintptr_t>(ws) & 255u)) return SPARGE_ERR_WORKSPACE;
+  return SPARGE_OK;
+}
+
+WindowParams window_params(const void* Q, const void* K, const void* V, const sparge_window_shape* s,
+                           const sparge_window* w, const int32_t* lens) {
+  WindowParams p{};
+  p.Q = static_cast<const __nv_bfloat16*>(Q);
+  p.K = static_cast<const __nv_bfloat16*>(K);
+  p.V = static_cast<const __nv_bfloat16*>(V);
+  p.lens = lens;
+  p.w = device_window(w);
+  p.H = s->H;
+  p.Hkv = s->Hkv;
+  p.N = s->N;
+  p.scale = (float)(1.0 / std::sqrt((double)s->d));
+  return p;
+}
+
+// ---------------------------------------------------------------- paged cache
+sparge_status check_cache(const sparge_cache* c, const sparge_cache_batch* b, CacheView* v) {
+  if (c == nullptr || b == nullptr) return SPARGE_ERR_INVALID_ARG;
+  if (c->pages <= 0 || c->Hkv <= 0 || c->page <= 0 || c->d <= 0 || b->B <= 0 || b->max_pages <= 0 || b->tokens < 0)
+    return SPARGE_ERR_INVALID_ARG;
+  if (c->type != SPARGE_CACHE_BF16 && c->type != SPARGE_CACHE_E4M3) return SPARGE_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return SPARGE_ERR_UNSUPPORTED;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return SPARGE_ERR_UNSUPPORTED;
+  if (!all_aligned16({c->k, c->v})) return SPARGE_ERR_INVALID_ARG;
+  if (c->type == SPARGE_CACHE_E4M3 && (c->k_exp == nullptr || c->v_exp == nullptr)) return SPARGE_ERR_INVALID_ARG;
+  if (!b->page_table || !b->first || !b->cu) return SPARGE_ERR_INVALID_ARG;
+  if ((int64_t)c->pages * c->Hkv > INT32_MAX || c->Hkv > 65535) return SPARGE_ERR_UNSUPPORTED;
+  if ((int64_t)b->tokens * c->Hkv * 2 > INT32_MAX) return SPARGE_ERR_UNSUPPORTED;
+  v->k = static_cast<uint8_t*>(c->k);
+  v->v = static_cast<uint8_t*>(c->v);
+  v->k_exp = c->k_exp;
+  v->v_exp = c->v_exp;
+  v->table = b->page_table;
+  v->first = b->first;
+  v->cu = b->cu;
+  v->pages = c->pages;
+  v->Hkv = c->Hkv;
+  v->page_shift = c->page == 16 ? 4 : c->page == 32 ? 5 : c->page == 64 ? 6 : 7;
+  v->B = b->B;
+  v->max_pages = b->max_pages;
+  v->tokens = b->tokens;
+  return SPARGE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sparge_window_workspace_bytes(int op, const sparge_window_shape* shape, const sparge_window* window) {
+  WDims dm;
+  if (check_window(shape, window, &dm) != SPARGE_OK) return 0;
+  return window_ws(op, dm);
+}
+
+sparge_status sparge_window_fwd(const void* Q, const void* K, const void* V, const sparge_window_shape* shape,
+                                const sparge_window* window, const int32_t* lens, void* O, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  WDims dm;
+  sparge_status st = check_window(shape, window, &dm);
+  if (st != SPARGE_OK) return st;
+  if (!all_aligned16({Q, K, V, O})) return SPARGE_ERR_INVALID_ARG;
+  st = check_ws(workspace, workspace_bytes, window_ws(SPARGE_OP_WINDOW_FWD, dm));
+  if (st != SPARGE_OK) return st;
+  WindowParams p = window_params(Q, K, V, shape, window, lens);
+  p.O = static_cast<__nv_bfloat16*>(O);
+  p.lse = lse;
+  const unsigned grid = (unsigned)ceil_div(dm.rows, 4);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (shape->d == 64) window_fwd_simple<64><<<grid, 128, 0, s>>>(p, dm.rows);
+  else window_fwd_simple<128><<<grid, 128, 0, s>>>(p, dm.rows);
+  return cuda_status(cudaGetLastError());
+}
+
+sparge_status sparge_window_bwd(const void* Q, const void* K, const void* V, const sparge_window_shape* shape,
+                                const sparge_window* window, const int32_t* lens, const void* O, const float* lse,
+                                const void* dO, void* dQ, void* dK, void* dV, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  WDims dm;
+  sparge_status st = check_window(shape, window, &dm);
+  if (st != SPARGE_OK) return st;
+  if (!all_aligned16({Q, K, V, O, dO, dQ, dK, dV}) || !lse) return SPARGE_ERR_INVALID_ARG;
+  st = check_ws(workspace, workspace_bytes, window_ws(SPARGE_OP_WINDOW_BWD, dm));
+  if (st != SPARGE_OK) return st;
+  WindowParams p = window_params(Q, K, V, shape, window, lens);
+  p.O_in = static_cast<const __nv_bfloat16*>(O);
+  p.dO = static_cast<const __nv_bfloat16*>(dO);
+  p.lse_in = lse;
+  p.dsum = static_cast<float*>(workspace);
+  p.dQ = static_cast<__nv_bfloat16*>(dQ);
+  p.dK = static_cast<__nv_bfloat16*>(dK);
+  p.dV = static_cast<__nv_bfloat16*>(dV);
+  const unsigned gq = (unsigned)ceil_div(dm.rows, 4), gk = (unsigned)ceil_div(dm.keys, 4);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (shape->d == 64) {
+    window_dq_simple<64><<<gq, 128, 0, s>>>(p, dm.rows);
+    window_dkdv_simple<64><<<gk, 128, 0, s>>>(p, dm.keys);
+  } else {
+    window_dq_simple<128><<<gq, 128, 0, s>>>(p, dm.rows);
+    window_dkdv_simple<128><<<gk, 128, 0, s>>>(p, dm.keys);
+  }
+  return cuda_status(cudaGetLastError());
+}
+
+sparge_status sparge_cache_write(const sparge_cache* cache, const sparge_cache_batch* batch, const void* K,
+                                 int64_t k_stride, const void* V, int64_t v_stride, void* stream) {
+  CacheView v;
+  sparge_status st = check_cache(cache, batch, &v);
+  if (st != SPARGE_OK) return st;
+  if (batch->tokens == 0) return SPARGE_OK;
+  const int64_t least = (int64_t)cache->Hkv * cache->d;
+  if (!all_aligned16({K, V}) || k_stride < least || v_stride < least || k_stride % 8 || v_stride % 8)
+    return SPARGE_ERR_INVALID_ARG;
+  const __nv_bfloat16 *k = static_cast<const __nv_bfloat16*>(K), *vv = static_cast<const __nv_bfloat16*>(V);
+  const unsigned grid = (unsigned)ceil_div((int64_t)batch->tokens * cache->Hkv * 2, 256 / (cache->d / 8));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool q = cache->type == SPARGE_CACHE_E4M3;
+  if (cache->d == 64) {
+    if (q) cache_write_kernel<64, true><<<grid, 256, 0, s>>>(v, k, k_stride, vv, v_stride);
+    else cache_write_kernel<64, false><<<grid, 256, 0, s>>>(v, k, k_stride, vv, v_stride);
+  } else {
+    if (q) cache_write_kernel<128, true><<<grid, 256, 0, s>>>(v, k, k_stride, vv, v_stride);
+    else cache_write_kernel<128, false><<<grid, 256, 0, s>>>(v, k, k_stride, vv, v_stride);
+  }
+  return cuda_status(cudaGetLastError());
+}
+
+sparge_status sparge_cache_read(const sparge_cache* cache, const sparge_cache_batch* batch, void* K, void* V,
+                                void* stream) {
+  CacheView v;
+  sparge_status st = check_cache(cache, batch, &v);
+  if (st != SPARGE_OK) return st;
+  if (batch->tokens == 0) return SPARGE_OK;
+  if (!all_aligned16({K, V})) return SPARGE_ERR_INVALID_ARG;
+  __nv_bfloat16 *k = static_cast<__nv_bfloat16*>(K), *vv = static_cast<__nv_bfloat16*>(V);
+  const unsigned grid = (unsigned)ceil_div((int64_t)batch->tokens * cache->Hkv * 2, 256 / (cache->d / 8));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool q = cache->type == SPARGE_CACHE_E4M3;
+  if (cache->d == 64) {
+    if (q) cache_read_kernel<64, true><<<grid, 256, 0, s>>>(v, k, vv);
+    else cache_read_kernel<64, false><<<grid, 256, 0, s>>>(v, k, vv);
+  } else {
+    if (q) cache_read_kernel<128, true><<<grid, 256, 0, s>>>(v, k, vv);
+    else cache_read_kernel<128, false><<<grid, 256, 0, s>>>(v, k, vv);
+  }
+  return cuda_status(cudaGetLastError());
+}
+
+size_t sparge_cache_attn_workspace_bytes(const sparge_cache* cache, const sparge_cache_batch* batch, int32_t H,
+                                         int32_t max_new, int32_t max_len, const sparge_window* window) {
+  (void)cache, (void)batch, (void)H, (void)max_new, (void)max_len, (void)window;
+  return 0;
+}
+
+sparge_status sparge_cache_attn(const sparge_cache* cache, const sparge_cache_batch* batch, const void* Q,
+                                int64_t q_stride, int32_t H, int32_t max_new, int32_t max_len,
+                                const sparge_window* window, void* O, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  CacheAttnParams p{};
+  sparge_status st = check_cache(cache, batch, &p.c);
+  if (st != SPARGE_OK) return st;
+  if (!window_ok(window) || H <= 0 || H % cache->Hkv || max_new < 1 || max_len < 1) return SPARGE_ERR_INVALID_ARG;
+  if ((int64_t)batch->tokens * H > INT32_MAX) return SPARGE_ERR_UNSUPPORTED;
+  if (batch->tokens == 0) return SPARGE_OK;
+  if (!all_aligned16({Q, O}) || q_stride < (int64_t)H * cache->d || q_stride % 8) return SPARGE_ERR_INVALID_ARG;
+  st = check_ws(workspace, workspace_bytes,
+                sparge_cache_attn_workspace_bytes(cache, batch, H, max_new, max_len, window));
+  if (st != SPARGE_OK) return st;
+  p.w = device_window(window);
+  p.Q = static_cast<const __nv_bfloat16*>(Q);
+  p.q_stride = q_stride;
+  p.O = static_cast<__nv_bfloat16*>(O);
+  p.lse = lse;
+  p.H = H;
+  p.scale = (float)(1.0 / std::sqrt((double)cache->d));
+  const unsigned grid = (unsigned)ceil_div((int64_t)batch->tokens * H, 4);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool q = cache->type == SPARGE_CACHE_E4M3;
+  if (cache->d == 64) {
+    if (q) cache_attn_simple<64, true><<<grid, 128, 0, s>>>(p);
+    else cache_attn_simple<64, false><<<grid, 128, 0, s>>>(p);
+  } else {
+    if (q) cache_attn_simple<128, true><<<grid, 128, 0, s>>>(p);
+    else cache_attn_simple<128, false><<<grid, 128, 0, s>>>(p);
+  }
+  return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -21,6 +22,8 @@ _lib = ctypes.CDLL(_LIB_PATH)
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_TIMEOUT = range(6)
 OP_MASK, OP_ATTN, OP_SLA2, OP_ATTN_Q8, OP_MASK_ROUTER, OP_ATTN_BWD, OP_SLA2_BWD = 0, 1, 2, 3, 4, 5, 6
+OP_WINDOW_FWD, OP_WINDOW_BWD = 7, 8
+CACHE_BF16, CACHE_E4M3 = 0, 1
 
 # Kernel launches per call of each entry point (for launch accounting).
 MASK_LAUNCHES, ATTN_LAUNCHES, SLA2_LAUNCHES, Q8_LAUNCHES, ROUTER_LAUNCHES, BWD_LAUNCHES = 3, 1, 4, 3, 5, 4
@@ -32,7 +35,9 @@ SLA2_BWD_LAUNCHES = 12
 # Every symbol the header declares.
 EXPORTS = ("sparge_workspace_bytes", "sparge_mask", "sparge_attn_fwd", "sla2_attn_fwd",
            "sparge_device_status", "sparge_status_string", "sparge_mask_noalloc", "sparge_attn_fwd_q8",
-           "sparge_mask_router", "sparge_attn_bwd", "sla2_attn_bwd", "sparge_selftest_wait")
+           "sparge_mask_router", "sparge_attn_bwd", "sla2_attn_bwd", "sparge_selftest_wait",
+           "sparge_window_workspace_bytes", "sparge_window_fwd", "sparge_window_bwd", "sparge_cache_write",
+           "sparge_cache_read", "sparge_cache_attn_workspace_bytes", "sparge_cache_attn")
 
 
 def order_launches(shape) -> int:
@@ -43,6 +48,24 @@ def order_launches(shape) -> int:
 
 class Shape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "H", "N", "d", "bq", "bk")]
+
+
+class WindowShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "H", "Hkv", "N", "d")]
+
+
+class Window(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("left", "right", "sinks", "unit")]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_exp", "v_exp")] + [
+        (n, ctypes.c_int32) for n in ("pages", "Hkv", "page", "d", "type")]
+
+
+class CacheBatch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("page_table", "first", "cu")] + [
+        (n, ctypes.c_int32) for n in ("B", "max_pages", "tokens")]
 
 
 _vp, _sz, _dbl = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_double
@@ -64,6 +87,18 @@ _lib.sparge_device_status.argtypes = [_vp, ctypes.POINTER(ctypes.c_int32)]
 _lib.sparge_selftest_wait.argtypes = [ctypes.c_int32, _vp, _vp]
 _lib.sparge_status_string.argtypes = [ctypes.c_int]
 _lib.sparge_status_string.restype = ctypes.c_char_p
+_i32, _i64 = ctypes.c_int32, ctypes.c_int64
+_lib.sparge_window_workspace_bytes.argtypes = [ctypes.c_int, _vp, _vp]
+_lib.sparge_window_workspace_bytes.restype = _sz
+_lib.sparge_window_fwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.sparge_window_bwd.argtypes = [_vp] * 13 + [_sz, _vp]
+_lib.sparge_cache_write.argtypes = [_vp, _vp, _vp, _i64, _vp, _i64, _vp]
+_lib.sparge_cache_read.argtypes = [_vp, _vp, _vp, _vp, _vp]
+_lib.sparge_cache_attn_workspace_bytes.argtypes = [_vp, _vp, _i32, _i32, _i32, _vp]
+_lib.sparge_cache_attn_workspace_bytes.restype = _sz
+_lib.sparge_cache_attn.argtypes = [_vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]
+for _f in ("sparge_window_fwd", "sparge_window_bwd", "sparge_cache_write", "sparge_cache_read", "sparge_cache_attn"):
+    getattr(_lib, _f).restype = ctypes.c_int
 for _f in ("sparge_mask", "sparge_mask_router", "sparge_attn_bwd", "sla2_attn_bwd", "sparge_attn_fwd", "sla2_attn_fwd", "sparge_device_status", "sparge_attn_fwd_q8",
            "sparge_selftest_wait"):
     getattr(_lib, _f).restype = ctypes.c_int
@@ -291,3 +326,224 @@ def device_status(stream=None) -> int:
     if rc not in (OK, ERR_DEVICE_TIMEOUT):
         raise SpargeError(rc, "sparge_device_status")
     return int(code.value)
+
+
+# ---------------------------------------------------------------------------
+# Windowed attention and the paged cache. A single token's call takes a few
+# microseconds on the GPU, so these bindings look at each argument once, pack
+# the C structs in one go and hand plain addresses over.
+# ---------------------------------------------------------------------------
+_pack_wshape = struct.Struct("5i").pack
+_pack_window = struct.Struct("4i").pack
+_pack_cache = struct.Struct("4P5i4x").pack
+_pack_batch = struct.Struct("3P3i4x").pack
+_BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+
+
+class _on:
+    """The stream to launch on (a raw handle) for tensors of `device`; makes that device current meanwhile."""
+
+    __slots__ = ("handle", "guard", "foreign")
+
+    def __init__(self, device, stream):
+        index = device.index
+        current = torch.cuda.current_device()
+        if stream is None:
+            self.handle, self.foreign = torch.cuda.current_stream(index).cuda_stream, None
+        else:
+            if stream.device.index != index:
+                raise ValueError("the stream belongs to another device than the tensors")
+            self.handle = stream.cuda_stream
+            self.foreign = None if self.handle == torch.cuda.current_stream(index).cuda_stream else stream
+        self.guard = None if index == current else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def keep(self, *tensors):
+        """Memory taken here for a stream that is not the current one is not handed out again before that stream is done."""
+        if self.foreign is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.foreign)
+
+
+def _want(t, name, dtype, shape, device):
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _window_args(Q, K, V, left, right, sinks, unit, lens):
+    if Q.dtype != _BF16 or not Q.is_cuda or Q.dim() != 4 or not Q.is_contiguous() or K.dim() != 4:
+        raise ValueError("Q, K, V must be contiguous bf16 CUDA tensors of shape [B,H,N,d] and [B,Hkv,N,d]")
+    B, H, N, d = Q.shape
+    Hkv = K.shape[1]
+    kv, device = (B, Hkv, N, d), Q.device
+    _want(K, "K", _BF16, kv, device)
+    _want(V, "V", _BF16, kv, device)
+    plens = None if lens is None else _want(lens, "lens", _I32, (B,), device)
+    return _pack_wshape(B, H, Hkv, N, d), _pack_window(left, right, sinks, unit), plens, kv, device
+
+
+def sparge_window_fwd(Q, K, V, left: int, right: int, sinks: int = 0, unit: int = 1, lens=None, O=None, lse=None,
+                      workspace=None, stream=None):
+    """Attention with a sliding window and sinks over [B,H,N,d] (K, V: [B,Hkv,N,d]); left and right count units of
+    `unit` tokens, -1 for no limit; lens: int32 [B] lengths of a padded batch. Returns O (and fills lse if given)."""
+    shape, window, plens, _, device = _window_args(Q, K, V, left, right, sinks, unit, lens)
+    on = _on(device, stream)
+    if O is None:
+        O = torch.empty_like(Q)
+        on.keep(O)
+    else:
+        _want(O, "O", _BF16, Q.shape, device)
+    plse = None if lse is None else _want(lse, "lse", _F32, Q.shape[:3], device)
+    ws, nws = _window_ws(OP_WINDOW_FWD, shape, window, workspace, device, on)
+    with on as handle:
+        rc = _lib.sparge_window_fwd(Q.data_ptr(), K.data_ptr(), V.data_ptr(), shape, window, plens, O.data_ptr(), plse,
+                                    ws, nws, handle)
+    _check(rc, "sparge_window_fwd")
+    return O
+
+
+def _window_ws(op, shape, window, workspace, device, on):
+    if workspace is None:
+        n = _lib.sparge_window_workspace_bytes(op, shape, window)
+        if n == 0:
+            return None, 0
+        workspace = torch.empty(n, dtype=_U8, device=device)
+        on.keep(workspace)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def sparge_window_bwd(Q, K, V, O, lse, dO, left: int, right: int, sinks: int = 0, unit: int = 1, lens=None, dQ=None,
+                      dK=None, dV=None, workspace=None, stream=None):
+    """Gradients of sparge_window_fwd (O and lse from that call) for dL/dO = dO. Returns (dQ, dK, dV)."""
+    shape, window, plens, kv, device = _window_args(Q, K, V, left, right, sinks, unit, lens)
+    for t, name in ((O, "O"), (dO, "dO")):
+        _want(t, name, _BF16, Q.shape, device)
+    plse = _want(lse, "lse", _F32, Q.shape[:3], device)
+    on = _on(device, stream)
+    made = []
+    out = []
+    for t, like, name in ((dQ, Q, "dQ"), (dK, K, "dK"), (dV, V, "dV")):
+        if t is None:
+            t = torch.empty_like(like)
+            made.append(t)
+        else:
+            _want(t, name, _BF16, like.shape, device)
+        out.append(t)
+    on.keep(*made)
+    ws, nws = _window_ws(OP_WINDOW_BWD, shape, window, workspace, device, on)
+    with on as handle:
+        rc = _lib.sparge_window_bwd(Q.data_ptr(), K.data_ptr(), V.data_ptr(), shape, window, plens, O.data_ptr(), plse,
+                                    dO.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws, nws,
+                                    handle)
+    _check(rc, "sparge_window_bwd")
+    return tuple(out)
+
+
+def _cache_args(k_pages, v_pages, k_exp, v_exp, page_table, first, cu, tokens):
+    """The two C structs of a paged cache and a batch of its sequences."""
+    if not k_pages.is_cuda or k_pages.dim() != 4:
+        raise ValueError("the cache's pages must be CUDA tensors of shape [pages, Hkv, page, d]")
+    device, dtype, shape = k_pages.device, k_pages.dtype, k_pages.shape
+    pk, pv = _want(k_pages, "k_pages", dtype, shape, device), _want(v_pages, "v_pages", dtype, shape, device)
+    if dtype == _BF16:
+        kind, ek, ev = CACHE_BF16, 0, 0
+        if k_exp is not None or v_exp is not None:
+            raise ValueError("a bf16 cache has no exponents")
+    elif dtype == _E4M3:
+        if k_exp is None or v_exp is None:
+            raise ValueError("an e4m3 cache needs k_exp and v_exp")
+        kind = CACHE_E4M3
+        ek, ev = _want(k_exp, "k_exp", _U8, shape[:3], device), _want(v_exp, "v_exp", _U8, shape[:3], device)
+    else:
+        raise ValueError("a cache holds bfloat16 or float8_e4m3fn")
+    if page_table.dim() != 2 or page_table.dtype != _I32:
+        raise ValueError("page_table must be an int32 tensor of shape [B, max_pages]")
+    B, most = page_table.shape
+    pt = _want(page_table, "page_table", _I32, (B, most), device)
+    pf, pc = _want(first, "first", _I32, (B,), device), _want(cu, "cu", _I32, (B + 1,), device)
+    return _pack_cache(pk, pv, ek, ev, *shape, kind), _pack_batch(pt, pf, pc, B, most, tokens), device
+
+
+def _token_rows(t, name, heads, d, device):
+    """Address and token stride of packed tokens [T, heads, d]: heads and channels contiguous, tokens any stride."""
+    if t.dtype != _BF16 or t.device != device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or (
+            t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d))):
+        raise ValueError(f"{name} must be a bf16 tensor of shape [tokens, {heads}, {d}] on {device}, contiguous within a token")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * d
+
+
+def sparge_cache_write(k, v, k_pages, v_pages, page_table, first, cu_new, k_exp=None, v_exp=None, stream=None) -> None:
+    """Writes new tokens' k, v (bf16 [T,Hkv,d], any token stride) into the paged cache at positions first[b], ..."""
+    cache, batch, device = _cache_args(k_pages, v_pages, k_exp, v_exp, page_table, first, cu_new, k.shape[0])
+    _, Hkv, _, d = k_pages.shape
+    pk, sk = _token_rows(k, "k", Hkv, d, device)
+    pv, sv = _token_rows(v, "v", Hkv, d, device)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must hold the same tokens")
+    with _on(device, stream) as handle:
+        rc = _lib.sparge_cache_write(cache, batch, pk, sk, pv, sv, handle)
+    _check(rc, "sparge_cache_write")
+
+
+def sparge_cache_read(k_pages, v_pages, page_table, first, cu, tokens: int, k_exp=None, v_exp=None, K=None, V=None,
+                      stream=None):
+    """The batch's positions first[b], ... (cu[b+1] - cu[b] of them, `tokens` rows in all) as bf16 (K, V) [tokens,Hkv,d]."""
+    cache, batch, device = _cache_args(k_pages, v_pages, k_exp, v_exp, page_table, first, cu, tokens)
+    shape = (tokens, k_pages.shape[1], k_pages.shape[3])
+    on = _on(device, stream)
+    out = []
+    for t, name in ((K, "K"), (V, "V")):
+        if t is None:
+            t = torch.empty(shape, dtype=_BF16, device=device)
+            on.keep(t)
+        else:
+            _want(t, name, _BF16, shape, device)
+        out.append(t)
+    with on as handle:
+        rc = _lib.sparge_cache_read(cache, batch, out[0].data_ptr(), out[1].data_ptr(), handle)
+    _check(rc, "sparge_cache_read")
+    return out[0], out[1]
+
+
+def sparge_cache_attn(Q, k_pages, v_pages, page_table, first, cu_new, max_new: int, max_len: int, left: int = -1,
+                      right: int = 0, sinks: int = 0, unit: int = 1, k_exp=None, v_exp=None, O=None, lse=None,
+                      workspace=None, stream=None):
+    """Attention of the new tokens Q (bf16 [T,H,d], any token stride), which stand at positions first[b], ... of their
+    sequences, over the paged cache that holds those positions already. max_new and max_len bound a sequence's new
+    tokens and its length. Returns O [T,H,d] (and fills lse [T,H] if given)."""
+    T, H, d = Q.shape
+    cache, batch, device = _cache_args(k_pages, v_pages, k_exp, v_exp, page_table, first, cu_new, T)
+    pq, sq = _token_rows(Q, "Q", H, k_pages.shape[3], device)
+    on = _on(device, stream)
+    if O is None:
+        O = torch.empty((T, H, d), dtype=_BF16, device=device)
+        on.keep(O)
+    else:
+        _want(O, "O", _BF16, Q.shape, device)
+    plse = None if lse is None else _want(lse, "lse", _F32, (T, H), device)
+    window = _pack_window(left, right, sinks, unit)
+    if workspace is None:
+        n = _lib.sparge_cache_attn_workspace_bytes(cache, batch, H, max_new, max_len, window)
+        if n:
+            workspace = torch.empty(n, dtype=_U8, device=device)
+            on.keep(workspace)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    ws, nws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    with on as handle:
+        rc = _lib.sparge_cache_attn(cache, batch, pq, sq, H, max_new, max_len, window, O.data_ptr(), plse, ws, nws,
+                                    handle)
+    _check(rc, "sparge_cache_attn")
+    return O

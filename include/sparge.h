@@ -93,7 +93,9 @@ enum {
   SPARGE_OP_ATTN_Q8 = 3,
   SPARGE_OP_MASK_ROUTER = 4,
   SPARGE_OP_ATTN_BWD = 5,
-  SPARGE_OP_SLA2_BWD = 6
+  SPARGE_OP_SLA2_BWD = 6,
+  SPARGE_OP_WINDOW_FWD = 7, /* sparge_window_workspace_bytes */
+  SPARGE_OP_WINDOW_BWD = 8  /* sparge_window_workspace_bytes */
 };
 
 /* Workspace bytes the operation needs for this shape (0 if none, or if the
@@ -274,6 +276,136 @@ sparge_status sparge_attn_fwd_q8(const void* Q, const void* K, const void* V, co
 sparge_status sla2_attn_fwd(const void* Q, const void* K, const void* V, const sparge_shape* shape,
                             const int32_t* kv_idx, const int32_t* kv_cnt, const float* alpha, void* O,
                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Windowed attention and the paged cache: a clip generated frame after frame
+ * attends to a window of frames and to the first ones, in training over the
+ * whole clip and in serving over a cache of the earlier tokens' K and V.
+ *
+ * Visibility. Positions are grouped into units of `unit` tokens (a frame; 1
+ * for single tokens). The row at position i sees the key at position j < L
+ * (L: the sequence's length) iff
+ *     j/unit <= i/unit + right        (right = -1: no limit), and
+ *     j/unit >= i/unit - left         (left = -1: no limit), or j < sinks
+ * with integer divisions: a window around the row, and the first `sinks`
+ * tokens as far as `right` lets the row see. right = 0 with unit = 1 is causal
+ * attention; right = 0 with unit = a frame's tokens is causal from frame to
+ * frame and bidirectional inside one. A row that sees nothing gets O = 0 and
+ * lse = -inf.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  int32_t left, right; /* units before and after the row's own; -1: no limit */
+  int32_t sinks;       /* tokens at the start that stay visible, >= 0 */
+  int32_t unit;        /* tokens per unit, >= 1 */
+} sparge_window;
+
+typedef struct {
+  int32_t B, H, Hkv, N, d; /* batch, query heads, K/V heads (a divisor of H), tokens, head dim (64 or 128) */
+} sparge_window_shape;
+
+/* Workspace bytes of SPARGE_OP_WINDOW_FWD / _BWD (0 if none or if the
+ * arguments are invalid). */
+size_t sparge_window_workspace_bytes(int op, const sparge_window_shape* shape, const sparge_window* window);
+
+/* Windowed attention forward over whole sequences.
+ *   O[b,h,i] = sum_j softmax_j(q_i . k_j / sqrt(d)) v_j over the keys visible
+ *              to i, K and V of head h / (H / Hkv); fp32 softmax and sums,
+ *              P rounded to bf16 for its product, O stored as bf16.
+ *   Q, O        bf16 [B,H,N,d];  K, V: bf16 [B,Hkv,N,d].
+ *   lens        optional int32 [B], device: L of each sequence, taken as
+ *               min(max(lens, 0), N). Rows at or past it get O = 0 and
+ *               lse = -inf; what Q, K and V hold there (NaN too) does not
+ *               matter. NULL: N for all.
+ *   lse         optional output, float [B,H,N], natural logarithm.
+ * Values at positions before L have to be finite: a key that one row of a
+ * tile sees and another does not reaches the latter as 0 * v.
+ * Limits: d 64 or 128, B * Hkv <= 65535. Workspace:
+ * sparge_window_workspace_bytes(SPARGE_OP_WINDOW_FWD, ...). */
+sparge_status sparge_window_fwd(const void* Q, const void* K, const void* V, const sparge_window_shape* shape,
+                                const sparge_window* window, const int32_t* lens, void* O, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Windowed attention backward: gradients of sparge_window_fwd for dL/dO = dO.
+ *   D_i = dO_i . O_i,  P_ij = exp(q_i . k_j / sqrt(d) - lse_i),
+ *   dS_ij = P_ij (dO_i . v_j - D_i) over the keys visible to i,
+ *   dQ_i = sum_j dS_ij k_j / sqrt(d),  dK_j = sum_i dS_ij q_i / sqrt(d),
+ *   dV_j = sum_i P_ij dO_i, the sums over i also over the heads that share K, V.
+ *   O, lse      the forward's, for the same inputs.
+ *   dO          bf16 [B,H,N,d];  dQ: bf16 [B,H,N,d];  dK, dV: bf16 [B,Hkv,N,d].
+ * Rows at or past L get zeros in dQ, dK and dV; what dO holds there does not
+ * matter. Precision: fp32 scores, P and dS rounded to bf16 for their products,
+ * fp32 sums, D_i from the bf16 O. No atomics: identical inputs give identical
+ * gradients. Workspace: sparge_window_workspace_bytes(SPARGE_OP_WINDOW_BWD, ...). */
+sparge_status sparge_window_bwd(const void* Q, const void* K, const void* V, const sparge_window_shape* shape,
+                                const sparge_window* window, const int32_t* lens, const void* O, const float* lse,
+                                const void* dO, void* dQ, void* dK, void* dV, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* A paged cache of K and V, owned by the caller. Position p of sequence b
+ * lies in page page_table[b][p / page] at place p % page.
+ *   k, v        [pages, Hkv, page, d]: bf16, or e4m3 codes.
+ *   k_exp, v_exp  e4m3 only: uint8 [pages, Hkv, page], the power of two of each
+ *               (token, head) row: value = code * 2^(byte - 127). Byte 255: the
+ *               row is NaN as a whole.
+ * A page id outside [0, pages), or a position past max_pages * page, is a place
+ * that does not exist: it is not written, reads back as 0, and no row sees it
+ * (a rolling cache drops a page by writing -1 into the table). */
+enum { SPARGE_CACHE_BF16 = 0, SPARGE_CACHE_E4M3 = 1 };
+
+typedef struct {
+  void *k, *v;
+  uint8_t *k_exp, *v_exp;
+  int32_t pages, Hkv, page, d; /* page: 16, 32, 64 or 128 tokens; d: 64 or 128 */
+  int32_t type;                /* SPARGE_CACHE_BF16 or SPARGE_CACHE_E4M3 */
+} sparge_cache;
+
+/* Tokens of a batch of sequences, packed: those of sequence b are rows
+ * cu[b] .. cu[b+1] - 1 of the token tensors and stand at the positions
+ * first[b], first[b] + 1, ... of its cache.
+ *   page_table  int32 [B, max_pages];  first: int32 [B], >= 0;
+ *   cu          int32 [B + 1], ascending from 0. All device memory.
+ * tokens is the token tensors' number of rows; rows at or past cu[B] are
+ * neither read nor written. */
+typedef struct {
+  const int32_t *page_table, *first, *cu;
+  int32_t B, max_pages, tokens;
+} sparge_cache_batch;
+
+/* Writes the new tokens' K and V into the cache.
+ *   K, V        bf16 [tokens, Hkv, d], token t's row at K + t * k_stride
+ *               (elements, a multiple of 8), heads contiguous.
+ * bf16: the values. e4m3, per (token, head): the largest magnitude a of its d
+ * channels is m * 2^k with 1 <= m < 2; the power is k - 8 if m <= 1.75, else
+ * k - 7 (the least that puts a at or below the type's 448), kept in
+ * [-117, 119]; code = e4m3(x / 2^power), nearest even, saturating. A power of
+ * two divides exactly, so a code is one rounding of x and reading it back is
+ * exact in bf16. A row holding a NaN or an infinity gets byte 255.
+ * Two tokens with the same place in the cache: either may end up there. */
+sparge_status sparge_cache_write(const sparge_cache* cache, const sparge_cache_batch* batch, const void* K,
+                                 int64_t k_stride, const void* V, int64_t v_stride, void* stream);
+
+/* Reads the batch's positions back as contiguous bf16 K, V [tokens, Hkv, d]. */
+sparge_status sparge_cache_read(const sparge_cache* cache, const sparge_cache_batch* batch, void* K, void* V,
+                                void* stream);
+
+/* Attention of new tokens over the cache, which holds them already
+ * (sparge_cache_write first): the row of sequence b's t-th new token stands at
+ * position first[b] + t, and L = first[b] + the number of its new tokens.
+ *   Q           bf16 [tokens, H, d], token t's row at Q + t * q_stride (elements,
+ *               a multiple of 8), heads contiguous.
+ *   H           query heads, a multiple of cache->Hkv.
+ *   max_new, max_len  bounds of a sequence's new tokens and of L, >= 1. They
+ *               choose how the work is split, not what is computed.
+ *   O           bf16 [tokens, H, d], contiguous;  lse: optional float [tokens, H].
+ * Precision as sparge_window_fwd; e4m3 rows enter the products as exact bf16.
+ * A place of the cache that no position of the batch stands for may hold
+ * anything, NaN too. Workspace: sparge_cache_attn_workspace_bytes(...). */
+size_t sparge_cache_attn_workspace_bytes(const sparge_cache* cache, const sparge_cache_batch* batch, int32_t H,
+                                         int32_t max_new, int32_t max_len, const sparge_window* window);
+sparge_status sparge_cache_attn(const sparge_cache* cache, const sparge_cache_batch* batch, const void* Q,
+                                int64_t q_stride, int32_t H, int32_t max_new, int32_t max_len,
+                                const sparge_window* window, void* O, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream);
 
 /* Reads and clears the device error word after synchronising the stream.
  * *code receives 0 if no kernel gave up a wait since the last call, else the
