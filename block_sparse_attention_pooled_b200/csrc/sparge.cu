@@ -25,6 +25,7 @@
 #include "window.cuh"
 #include "cache.cuh"
 #include "cache_attn.cuh"
+#include "wattn.cuh"
 
 namespace {
 

@@ -1,0 +1,439 @@
+// Windowed attention forward on the 5th-generation tensor cores, over whole
+// sequences and over the paged cache.
+//
+//   O_i = sum_j softmax_j(q_i . k_j / sqrt(d)) v_j over the keys visible to i,
+// in one pass over the keys with a running maximum and sum per row.
+//
+// One CTA per SM takes work items of 256 rows (two 128-row tiles A and B) of
+// one K/V head and walks the 128-key tiles that any of its rows may see: the
+// sinks below the window, then the window. Roles:
+//   warp 0       producer: Q, then K and V tiles into a ring, by TMA; a tile
+//                that reaches past the sequence's end (or into a page that is
+//                not there) is copied by the warp's lanes, zeros in the rows
+//                that do not exist, so that what memory holds there never
+//                meets a probability of 0;
+//   warp 1       MMA issuer and TMEM owner;
+//   warps 4..7   softmax of tile A: one row (TMEM lane) per thread;
+//   warps 8..11  softmax of tile B.
+// The two tiles alternate: while the tensor core works on one tile's products,
+// the other tile's softmax runs. Issue order per key tile:
+//   O_A += P_A(t) V(t); S_A(t+1) = Q_A K(t+1)^T; O_B += P_B(t) V(t); S_B(t+1).
+// The products complete in order, so "S(t+1) is there" also says that O(t) is,
+// and a row may be rescaled without a wait of its own.
+// TMEM columns: S_A [0,128), S_B [128,256), O_A [256,256+D), O_B [384,384+D);
+// P(t) (bf16, two per column) lies over the first 64 columns of its S(t).
+#pragma once
+#include <cuda.h>
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "attn.cuh"
+#include "cache.cuh"
+#include "ptx.cuh"
+#include "window.cuh"
+
+namespace sparge {
+
+enum : unsigned int {
+  kErrWinQ = 0x900, kErrWinQEmpty, kErrWinKvFull, kErrWinKvEmpty, kErrWinS, kErrWinP, kErrWinO, kErrWinOFree,
+  kErrWinDrain
+};
+
+constexpr int kWTile = 128;       // rows per tile and keys per tile
+constexpr int kWThreads = 384;
+
+struct WAttnParams {
+  Window w;
+  const int32_t* lens;  // whole sequences: [B] or null
+  __nv_bfloat16* O;
+  float* lse;
+  const __nv_bfloat16 *K, *V;  // for the tiles that the lanes copy
+  int B, H, Hkv, N, items, rtiles;
+  float scale_log2;
+};
+
+template <int D>
+struct WSmem {
+  static constexpr int NS = D == 128 ? 5 : 8;
+  static constexpr int kTileBytes = kWTile * D * 2;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffKv = 2 * kTileBytes;
+  static constexpr int kOffBar = kOffKv + NS * kTileBytes;
+  static constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarKvFull = 2, kBarKvEmpty = 2 + NS, kBarS = 2 + 2 * NS,
+                       kBarP = 4 + 2 * NS, kBarO = 6 + 2 * NS, kBarOFree = 8 + 2 * NS, kBarDrain = 10 + 2 * NS;
+  static constexpr int kNumBars = 11 + 2 * NS;
+  static constexpr int kOffTmem = kOffBar + kNumBars * 8;
+  static constexpr int kBytes = kOffTmem + 16 + 1024;
+};
+
+// Copies a [128 keys][D] tile (64-column boxes, 128-byte swizzle) by a warp's
+// lanes; row r comes from src(r), zeros where that is null.
+template <int D, typename Src>
+__device__ __forceinline__ void copy_tile(uint32_t dst, int lane, Src src) {
+  constexpr int CH = D / 8;         // 16-byte pieces per row
+  constexpr int RPI = 32 / CH;      // rows per step
+  const int c = lane % CH;
+  const uint32_t box = dst + (c / 8) * (kWTile * 128);
+#pragma unroll 1
+  for (int r0 = 0; r0 < kWTile; r0 += 4 * RPI) {
+    uint4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const __nv_bfloat16* row = src(r0 + u * RPI + lane / CH);
+      x[u] = row ? *reinterpret_cast<const uint4*>(row + c * 8) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = r0 + u * RPI + lane / CH;
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + r * 128 + (((c % 8) ^ (r & 7)) * 16)),
+                   "r"(x[u].x), "r"(x[u].y), "r"(x[u].z), "r"(x[u].w)
+                   : "memory");
+    }
+  }
+  fence_async_smem();
+  __syncwarp();
+}
+
+// The key tiles of a work item: `ns` tiles from key 0 that hold the sinks
+// below `lo`, then tiles from `lo` on. A sink tile's keys at or past `cut` are
+// not its own: they belong to the window's tiles or to nobody.
+struct KeyTiles {
+  int ns, total, lo, cut;
+  __device__ __forceinline__ int key0(int t) const { return t < ns ? t * kWTile : lo + (t - ns) * kWTile; }
+};
+
+// lo: the first row's first key, rounded down to `align`; hi: the last row's end.
+__device__ __forceinline__ KeyTiles key_tiles(int lo, int hi, int sinks, int align_mask) {
+  KeyTiles k;
+  k.lo = lo & ~align_mask;
+  k.cut = min(min(sinks, hi), k.lo);
+  k.ns = (k.cut + kWTile - 1) / kWTile;
+  if (k.ns * kWTile >= k.lo) k.lo = k.cut = k.ns = 0;  // the sinks' tiles reach the window: one run of tiles
+  k.total = k.ns + (max(hi - k.lo, 0) + kWTile - 1) / kWTile;
+  return k;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
+  uint32_t v[2][16];
+  tmem_ld16(taddr, v[0]);
+  tmem_ld16(taddr + 16, v[1]);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) r[j] = __uint_as_float(v[j / 16][j % 16]);
+}
+
+// One softmax step of a row: 128 scores at taddr -> P (bf16 pairs) over them.
+// [a, e): the row's window relative to the tile, k: its sinks relative to it;
+// `whole`: every key of the tile is visible to every row of the warp.
+template <int D>
+__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, bool first, bool whole, int a, int e, int k,
+                                             float scale_log2, float& m_run, float& l_run) {
+  float s[kWTile];
+  {
+    uint32_t v[8][16];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) tmem_ld16(ts + 16 * c, v[c]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[16 * c + j] = __uint_as_float(v[c][j]);
+  }
+  if (!whole) {
+#pragma unroll
+    for (int j = 0; j < kWTile; ++j)
+      if (j >= e || (j < a && j >= k)) s[j] = -INFINITY;
+  }
+  float m8[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    m8[j] = fmaxf(s[j], s[8 + j]);
+#pragma unroll
+    for (int i = 2; i < 16; i += 2) m8[j] = fmax3(m8[j], s[8 * i + j], s[8 * i + 8 + j]);
+  }
+  const float top = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+  const float m_new = fmaxf(m_run, top * scale_log2);
+  if (first) {
+    m_run = m_new;
+  } else if (__any_sync(0xffffffffu, m_new > m_run + kRescaleThreshold)) {
+    // O and l hold sums of 2^(s - m_run): move them to the new reference. The
+    // TMEM access is the warp's, so all its rows move (by 1 where the maximum
+    // held; a row that has seen nothing has 0 to move).
+    const float f = m_new == -INFINITY ? 1.0f : ex2_approx(m_run - m_new);
+    rescale_row<D>(to, f);
+    l_run *= f;
+    m_run = m_new;
+  }
+  const float ref = m_run == -INFINITY ? 0.0f : m_run;
+  const uint64_t scale2 = f2(scale_log2, scale_log2), negm2 = f2(-ref, -ref);
+  uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float2 x = f2_split(fma2(f2(s[32 * c + 2 * j], s[32 * c + 2 * j + 1]), scale2, negm2));
+      const uint64_t ex = f2(ex2_approx(x.x), ex2_approx(x.y));
+      acc[j & 3] = add2(acc[j & 3], ex);
+      const float2 ev = f2_split(ex);
+      pk[j] = pack_bf16x2(ev.x, ev.y);
+    }
+    tmem_st16(ts + 16 * c, pk);
+  }
+  const float2 t = f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])));
+  l_run += t.x + t.y;
+  tmem_st_wait();
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWThreads, 1)
+    window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const WAttnParams p) {
+  using L = WSmem<D>;
+  constexpr int NS = L::NS;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* sgen = smem_raw + (sbase - raw);
+  const uint32_t sQ = sbase + L::kOffQ, sKv = sbase + L::kOffKv;
+  auto bar = [&](int i) { return sbase + L::kOffBar + 8u * (uint32_t)i; };
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sgen + L::kOffTmem);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + L::kOffTmem + 4);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) {
+      const bool rows = (i >= L::kBarP && i < L::kBarP + 2) || (i >= L::kBarOFree && i < L::kBarOFree + 2);
+      mbar_init(bar(i), rows ? 128 : 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(sbase + L::kOffTmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // The block's registers (384 x 168) are shared out anew: the first four
+  // warps keep 80 each, so that the softmax's eight can hold a row's 128 scores.
+  auto few_registers = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); };
+
+  // Work item `it`: rows [q0, q0 + 256) of head bh. The last rows come first:
+  // they see the most where the past is not limited.
+  const int BH = p.B * p.H;
+  auto item = [&](int it, int& bh, int& q0, int& len, KeyTiles& kt) {
+    bh = it % BH;
+    q0 = (p.rtiles - 1 - it / BH) * 2 * kWTile;
+    len = seq_len(p.lens, bh / p.H, p.N);
+    if (q0 >= len) {
+      kt.total = 0;
+      return;
+    }
+    const int last = min(q0 + 2 * kWTile, len) - 1;
+    kt = key_tiles(p.w.lo(q0), p.w.hi(last, len), p.w.sinks, 0);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    few_registers();
+    uint32_t n = 0, nq = 0;  // ring slots filled, items with work
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+      int bh, q0, len;
+      KeyTiles kt;
+      item(it, bh, q0, len, kt);
+      if (kt.total == 0) continue;
+      const int b = bh / p.H, kvh = b * p.Hkv + (bh % p.H) / (p.H / p.Hkv);
+      ok = nq == 0 || role_wait(bar(L::kBarQEmpty), (nq - 1) & 1, kErrWinQEmpty, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(L::kBarQFull), 2 * L::kTileBytes);
+        for (int h = 0; h < 2; ++h)
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sQ + h * L::kTileBytes + c * (kWTile * 128), &tmQ, bar(L::kBarQFull), c * 64, q0 + h * kWTile,
+                        bh);
+      }
+      ++nq;
+      for (int t = 0; ok && t < 2 * kt.total; ++t, ++n) {  // K(0), V(0), K(1), V(1), ...
+        const int slot = n % NS, key0 = kt.key0(t >> 1);
+        ok = n < NS || role_wait(bar(L::kBarKvEmpty + slot), (n / NS - 1) & 1, kErrWinKvEmpty, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t dst = sKv + slot * L::kTileBytes;
+        if (len < p.N && key0 + kWTile > len) {
+          const __nv_bfloat16* src = ((t & 1) ? p.V : p.K) + ((int64_t)kvh * p.N + key0) * D;
+          copy_tile<D>(dst, lane, [&](int r) { return key0 + r < len ? src + (int64_t)r * D : nullptr; });
+          if (lane == 0) mbar_arrive(bar(L::kBarKvFull + slot));
+        } else if (lane == 0) {
+          mbar_arrive_expect_tx(bar(L::kBarKvFull + slot), L::kTileBytes);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(dst + c * (kWTile * 128), (t & 1) ? &tmV : &tmK, bar(L::kBarKvFull + slot), c * 64, key0, kvh);
+        }
+      }
+    }
+    // Never leave with copies in flight.
+    if (lane == 0) {
+      if (nq) mbar_wait(bar(L::kBarQFull), (nq - 1) & 1, kErrWinQ);
+      for (uint32_t i = n > NS ? n - NS : 0; i < n; ++i)
+        mbar_wait(bar(L::kBarKvFull + i % NS), (i / NS) & 1, kErrWinKvFull);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    few_registers();
+    const bool leader = elect_one();
+    constexpr uint32_t idS = idesc_bf16_f32(kWTile, kWTile, false, false);
+    constexpr uint32_t idO = idesc_bf16_f32(kWTile, D, false, true);
+    const uint64_t dQ = sdesc_sw128(sQ, 16, 1024);
+    const uint64_t dKm = sdesc_sw128(sKv, 16, 1024);              // K-major (S = Q K^T)
+    const uint64_t dVm = sdesc_sw128(sKv, kWTile * 128, 1024);    // MN-major (O += P V)
+    auto wait = [&](int b, uint32_t parity, unsigned int site) {
+      return __all_sync(0xffffffffu, role_wait(bar(b), parity, site, abort_flag));
+    };
+    uint32_t n = 0, nq = 0, np = 0;  // ring slots used, items, key tiles
+    bool ok = true;
+    auto issue_s = [&](int x, int slot) {  // S_x = Q_x K^T
+      if (leader) {
+        const uint64_t q = dQ + (uint64_t)((x * L::kTileBytes) >> 4), k = dKm + (uint64_t)((slot * L::kTileBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = ((kk >> 2) * (kWTile * 128) + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + x * 128, q + o, k + o, idS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(bar(L::kBarS + x));
+      }
+      __syncwarp();
+    };
+    for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+      int bh, q0, len;
+      KeyTiles kt;
+      item(it, bh, q0, len, kt);
+      if (kt.total == 0) continue;
+      ok = wait(L::kBarQFull, nq & 1, kErrWinQ) && wait(L::kBarKvFull + n % NS, (n / NS) & 1, kErrWinKvFull);
+      if (!ok) break;
+      tc_fence_after();
+      issue_s(0, n % NS);
+      issue_s(1, n % NS);
+      if (leader) {
+        mma_commit(bar(L::kBarKvEmpty + n % NS));
+        if (kt.total == 1) mma_commit(bar(L::kBarQEmpty));
+      }
+      __syncwarp();
+      ++n;
+      for (int t = 0; ok && t < kt.total; ++t, ++np) {
+        const int vs = n % NS, ks = (n + 1) % NS;
+        const bool more = t + 1 < kt.total;
+        for (int x = 0; x < 2; ++x) {
+          if (x == 0) ok = wait(L::kBarKvFull + vs, (n / NS) & 1, kErrWinKvFull);
+          if (ok && t == 0 && nq > 0) ok = wait(L::kBarOFree + x, (nq - 1) & 1, kErrWinOFree);
+          ok = ok && wait(L::kBarP + x, np & 1, kErrWinP);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t v = dVm + (uint64_t)((vs * L::kTileBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kWTile / 16; ++kk)  // 16 keys = 2048 bytes of V = 8 columns of P
+              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, v + kk * 128, idO, (t > 0 || kk > 0) ? 1u : 0u);
+            if (x == 1) mma_commit(bar(L::kBarKvEmpty + vs));
+            if (!more) mma_commit(bar(L::kBarO + x));
+          }
+          __syncwarp();
+          if (more) {
+            if (x == 0) ok = wait(L::kBarKvFull + ks, ((n + 1) / NS) & 1, kErrWinKvFull);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(x, ks);
+            if (x == 1 && leader) {
+              mma_commit(bar(L::kBarKvEmpty + ks));
+              if (t + 2 == kt.total) mma_commit(bar(L::kBarQEmpty));
+            }
+            __syncwarp();
+          }
+        }
+        n += more ? 2 : 1;
+      }
+      ++nq;
+    }
+    // Every MMA issued has completed before TMEM is freed.
+    if (leader) mma_commit(bar(L::kBarDrain));
+    __syncwarp();
+    mbar_wait(bar(L::kBarDrain), 0, kErrWinDrain);
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax and epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int x = (warp - 4) / 4;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + x * 128 + lane_off, to = tmem + 256 + x * 128 + lane_off;
+    uint32_t nq = 0, np = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+      int bh, q0, len;
+      KeyTiles kt;
+      item(it, bh, q0, len, kt);
+      const int i = q0 + x * kWTile + r;
+      const bool live = i < len;
+      const int lo = live ? p.w.lo(i) : 0, hi = live ? p.w.hi(i, len) : 0;
+      // Keys that all rows of the warp see without looking at the sinks.
+      const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
+      float m_run = -INFINITY, l_run = 0.0f;
+      for (int t = 0; t < kt.total; ++t, ++np) {
+        const int key0 = kt.key0(t);
+        ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarS + x), np & 1, kErrWinS, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        const bool sink = t < kt.ns;
+        const bool whole = sink ? key0 + kWTile <= min(kt.cut, all_hi) : key0 >= all_lo && key0 + kWTile <= all_hi;
+        const int e = (sink ? min(hi, kt.cut) : hi) - key0;
+        softmax_tile<D>(ts, to, t == 0, whole, sink ? 0 : lo - key0, e, p.w.sinks - key0, p.scale_log2, m_run, l_run);
+        tc_fence_before();
+        mbar_arrive(bar(L::kBarP + x));
+      }
+      if (!ok) break;
+      const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
+      if (kt.total > 0) {
+        ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarO + x), nq & 1, kErrWinO, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        ++nq;
+      }
+      __nv_bfloat16* out = p.O + ((int64_t)bh * p.N + i) * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (kt.total > 0) {
+          tmem_ld32(to + c, o);
+          tmem_ld_wait();
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          w[j] = kt.total > 0 && l_run > 0.0f ? pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv) : 0u;
+        if (i < p.N) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(out + c + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        }
+      }
+      if (kt.total > 0) {
+        tc_fence_before();
+        mbar_arrive(bar(L::kBarOFree + x));
+      }
+      if (p.lse != nullptr && i < p.N)
+        p.lse[(int64_t)bh * p.N + i] = l_run > 0.0f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+    }
+  } else {
+    few_registers();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace sparge

@@ -58,6 +58,49 @@ WindowParams window_params(const void* Q, const void* K, const void* V, const sp
   return p;
 }
 
+// SMs of the current device.
+int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+    known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+template <int D>
+sparge_status launch_window_fwd(const void* Q, const void* K, const void* V, const sparge_window_shape* s,
+                                const sparge_window* w, const int32_t* lens, void* O, float* lse, const WDims& dm,
+                                void* stream) {
+  CUtensorMap mq, mk, mv;
+  if (!make_map_bhnd(&mq, Q, dm.BH, s->N, D, kWTile) || !make_map_bhnd(&mk, K, dm.BHkv, s->N, D, kWTile) ||
+      !make_map_bhnd(&mv, V, dm.BHkv, s->N, D, kWTile))
+    return SPARGE_ERR_CUDA;
+  WAttnParams p{};
+  p.w = device_window(w);
+  p.lens = lens;
+  p.O = static_cast<__nv_bfloat16*>(O);
+  p.lse = lse;
+  p.K = static_cast<const __nv_bfloat16*>(K);
+  p.V = static_cast<const __nv_bfloat16*>(V);
+  p.B = s->B;
+  p.H = s->H;
+  p.Hkv = s->Hkv;
+  p.N = s->N;
+  p.rtiles = (int)ceil_div(s->N, 2 * kWTile);
+  if (dm.BH * p.rtiles > INT32_MAX / 2) return SPARGE_ERR_UNSUPPORTED;
+  p.items = (int)(dm.BH * p.rtiles);
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
+  cudaError_t e = ensure_smem(window_fwd_kernel<D>, WSmem<D>::kBytes, D == 64 ? 20 : 21);
+  if (e != cudaSuccess) return cuda_status(e);
+  window_fwd_kernel<D><<<std::min(p.items, sm_count()), kWThreads, WSmem<D>::kBytes,
+                         static_cast<cudaStream_t>(stream)>>>(mq, mk, mv, p);
+  return cuda_status(cudaGetLastError());
+}
+
 // ---------------------------------------------------------------- paged cache
 sparge_status check_cache(const sparge_cache* c, const sparge_cache_batch* b, CacheView* v) {
   if (c == nullptr || b == nullptr) return SPARGE_ERR_INVALID_ARG;
@@ -106,14 +149,8 @@ sparge_status sparge_window_fwd(const void* Q, const void* K, const void* V, con
   if (!all_aligned16({Q, K, V, O})) return SPARGE_ERR_INVALID_ARG;
   st = check_ws(workspace, workspace_bytes, window_ws(SPARGE_OP_WINDOW_FWD, dm));
   if (st != SPARGE_OK) return st;
-  WindowParams p = window_params(Q, K, V, shape, window, lens);
-  p.O = static_cast<__nv_bfloat16*>(O);
-  p.lse = lse;
-  const unsigned grid = (unsigned)ceil_div(dm.rows, 4);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (shape->d == 64) window_fwd_simple<64><<<grid, 128, 0, s>>>(p, dm.rows);
-  else window_fwd_simple<128><<<grid, 128, 0, s>>>(p, dm.rows);
-  return cuda_status(cudaGetLastError());
+  if (shape->d == 64) return launch_window_fwd<64>(Q, K, V, shape, window, lens, O, lse, dm, stream);
+  return launch_window_fwd<128>(Q, K, V, shape, window, lens, O, lse, dm, stream);
 }
 
 sparge_status sparge_window_bwd(const void* Q, const void* K, const void* V, const sparge_window_shape* shape,
