@@ -121,6 +121,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
   for (int j = 0; j < 32; ++j) r[j] = __uint_as_float(v[j / 16][j % 16]);
 }
 
+// Bits 0 .. n - 1 (n at most 0: none, 32 or more: all).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+}
+
 // One softmax step of a row: 128 scores at taddr -> P (bf16 pairs) over them.
 // [a, e): the row's window relative to the tile, k: its sinks relative to it;
 // `whole`: every key of the tile is visible to every row of the warp.
@@ -139,9 +144,14 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, bool firs
       for (int j = 0; j < 16; ++j) s[16 * c + j] = __uint_as_float(v[c][j]);
   }
   if (!whole) {
+    // One bit per key, 32 at a time: tests of single bits compile to selects,
+    // not to branches.
 #pragma unroll
-    for (int j = 0; j < kWTile; ++j)
-      if (j >= e || (j < a && j >= k)) s[j] = -INFINITY;
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t seen = bits_below(e - 32 * c) & (~bits_below(a - 32 * c) | bits_below(k - 32 * c));
+#pragma unroll
+      for (int j = 0; j < 32; ++j) s[32 * c + j] = (seen >> j) & 1u ? s[32 * c + j] : -INFINITY;
+    }
   }
   float m8[8];
 #pragma unroll
@@ -374,8 +384,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
       KeyTiles kt;
       item(it, bh, q0, len, kt);
       const int i = q0 + x * kWTile + r;
-      const bool live = i < len;
-      const int lo = live ? p.w.lo(i) : 0, hi = live ? p.w.hi(i, len) : 0;
+      // Rows past the end compute what the last row sees (so that no tile
+      // needs a mask for their sake) and store zeros.
+      const int at = max(min(i, len - 1), 0);
+      const int lo = p.w.lo(at), hi = p.w.hi(at, len);
       // Keys that all rows of the warp see without looking at the sinks.
       const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
       float m_run = -INFINITY, l_run = 0.0f;
@@ -392,6 +404,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         mbar_arrive(bar(L::kBarP + x));
       }
       if (!ok) break;
+      if (i >= len) l_run = 0.0f;
       const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
       if (kt.total > 0) {
         ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarO + x), nq & 1, kErrWinO, abort_flag));
