@@ -26,6 +26,7 @@
 #include "cache.cuh"
 #include "cache_attn.cuh"
 #include "wattn.cuh"
+#include "wattn_bwd.cuh"
 
 namespace {
 

@@ -33,29 +33,44 @@ bool all_aligned16(std::initializer_list<const void*> ps) {
   return true;
 }
 
-size_t window_ws(int op, const WDims& d) {
-  return op == SPARGE_OP_WINDOW_BWD ? align256((size_t)d.rows * 4) : 0;
+// How the rows of dK and dV's key tiles are split, from what the host knows.
+// A key that every later row sees (a sink, or any key where the past is not
+// limited) has up to N rows per head, another as many as the window is wide;
+// one CTA works through its rows in order, so long runs are cut into pieces of
+// at most about a third of an SM's share of the whole work (but of 8 tiles at
+// least: a piece's fp32 sums are written and read once more).
+struct KvSplit {
+  int tiles, sink_tiles, sink_pieces, pieces;
+  size_t slots;  // of [2][128][d] fp32
+};
+
+KvSplit kv_split(const sparge_window_shape* s, const sparge_window* w, const WDims& d) {
+  KvSplit k;
+  k.tiles = (int)ceil_div(s->N, kWTile);
+  const int64_t G = s->H / s->Hkv;
+  const int64_t reach = std::min<int64_t>(
+      s->N, w->left < 0 || w->right < 0 ? s->N : ((int64_t)w->left + w->right + 1) * w->unit + kWTile);
+  k.sink_tiles = w->left < 0 ? 0 : (int)ceil_div(std::min(w->sinks, s->N), kWTile);
+  const int64_t run = G * ceil_div(reach, kWTile), sink_run = G * k.tiles;
+  const int64_t all = d.BHkv * (run * (k.tiles - k.sink_tiles) + sink_run * k.sink_tiles);
+  const int64_t most = std::max<int64_t>(8, all / (3 * 148));
+  k.pieces = (int)std::min<int64_t>(ceil_div(run, most), 64);
+  k.sink_pieces = (int)std::min<int64_t>(ceil_div(sink_run, most), 64);
+  const size_t sinks = (size_t)d.BHkv * k.sink_tiles * k.sink_pieces;
+  k.slots = (k.sink_tiles > 0 && k.sink_pieces > 1) || k.pieces > 1 ? sinks : 0;
+  if (k.pieces > 1) k.slots += (size_t)d.BHkv * (k.tiles - k.sink_tiles) * k.pieces;
+  return k;
+}
+
+size_t window_ws(int op, const sparge_window_shape* s, const sparge_window* w, const WDims& d) {
+  if (op != SPARGE_OP_WINDOW_BWD) return 0;
+  return align256((size_t)d.rows * 4) + kv_split(s, w, d).slots * 2 * kWTile * s->d * 4;
 }
 
 sparge_status check_ws(const void* ws, size_t have, size_t need) {
   if (need == 0) return SPARGE_OK;
   if (ws == nullptr || have < need || (reinterpret_cast<uintptr_t>(ws) & 255u)) return SPARGE_ERR_WORKSPACE;
   return SPARGE_OK;
-}
-
-WindowParams window_params(const void* Q, const void* K, const void* V, const sparge_window_shape* s,
-                           const sparge_window* w, const int32_t* lens) {
-  WindowParams p{};
-  p.Q = static_cast<const __nv_bfloat16*>(Q);
-  p.K = static_cast<const __nv_bfloat16*>(K);
-  p.V = static_cast<const __nv_bfloat16*>(V);
-  p.lens = lens;
-  p.w = device_window(w);
-  p.H = s->H;
-  p.Hkv = s->Hkv;
-  p.N = s->N;
-  p.scale = (float)(1.0 / std::sqrt((double)s->d));
-  return p;
 }
 
 // SMs of the current device.
@@ -101,6 +116,64 @@ sparge_status launch_window_fwd(const void* Q, const void* K, const void* V, con
   return cuda_status(cudaGetLastError());
 }
 
+template <int D>
+sparge_status launch_window_bwd(const void* Q, const void* K, const void* V, const sparge_window_shape* s,
+                                const sparge_window* w, const int32_t* lens, const void* O, const float* lse,
+                                const void* dO, void* dQ, void* dK, void* dV, const WDims& dm, void* workspace,
+                                void* stream) {
+  CUtensorMap mq, mk, mv, mdo;
+  if (!make_map_bhnd(&mq, Q, dm.BH, s->N, D, kWTile) || !make_map_bhnd(&mk, K, dm.BHkv, s->N, D, kWTile) ||
+      !make_map_bhnd(&mv, V, dm.BHkv, s->N, D, kWTile) || !make_map_bhnd(&mdo, dO, dm.BH, s->N, D, kWTile))
+    return SPARGE_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  float* dsum = static_cast<float*>(workspace);
+  const KvSplit k = kv_split(s, w, dm);
+  WBwdParams p{};
+  p.w = device_window(w);
+  p.lens = lens;
+  p.Q = static_cast<const __nv_bfloat16*>(Q);
+  p.K = static_cast<const __nv_bfloat16*>(K);
+  p.V = static_cast<const __nv_bfloat16*>(V);
+  p.dO = static_cast<const __nv_bfloat16*>(dO);
+  p.lse = lse;
+  p.dsum = dsum;
+  p.dQ = static_cast<__nv_bfloat16*>(dQ);
+  p.dK = static_cast<__nv_bfloat16*>(dK);
+  p.dV = static_cast<__nv_bfloat16*>(dV);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256((size_t)dm.rows * 4));
+  p.B = s->B;
+  p.H = s->H;
+  p.Hkv = s->Hkv;
+  p.N = s->N;
+  p.rtiles = k.tiles;
+  p.sink_tiles = k.sink_tiles;
+  p.sink_pieces = k.sink_pieces;
+  p.pieces = k.pieces;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
+  p.scale = (float)(1.0 / std::sqrt((double)D));
+  const int64_t gq = dm.BH * k.tiles;
+  const int64_t gk = dm.BHkv * ((int64_t)k.sink_tiles * k.sink_pieces + (int64_t)(k.tiles - k.sink_tiles) * k.pieces);
+  if (gq > INT32_MAX || gk > INT32_MAX) return SPARGE_ERR_UNSUPPORTED;
+  bwd_dot_kernel<D><<<(unsigned)ceil_div(dm.rows, 256 / (D / 8)), 256, 0, st>>>(
+      static_cast<const __nv_bfloat16*>(O), p.dO, dm.rows, dsum);
+  cudaError_t e = ensure_smem(window_dq_kernel<D>, WDqSmem<D>::kBytes, D == 64 ? 22 : 23);
+  if (e != cudaSuccess) return cuda_status(e);
+  window_dq_kernel<D><<<(unsigned)gq, kWThreads, WDqSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, p);
+  e = ensure_smem(window_dkdv_kernel<D>, WDkvSmem<D>::kBytes, D == 64 ? 24 : 25);
+  if (e != cudaSuccess) return cuda_status(e);
+  window_dkdv_kernel<D><<<(unsigned)gk, kWThreads, WDkvSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, p);
+  for (int c = 0; c < 2; ++c) {
+    const int pieces = c == 0 ? k.sink_pieces : k.pieces, tile0 = c == 0 ? 0 : k.sink_tiles;
+    const int tiles = c == 0 ? k.sink_tiles : k.tiles - k.sink_tiles;
+    if (pieces <= 1 || tiles == 0) continue;
+    const float* part = p.part + (c == 0 ? 0 : (size_t)dm.BHkv * k.sink_tiles * k.sink_pieces * 2 * kWTile * D);
+    const int64_t quads = dm.BHkv * tiles * 2 * kWTile * (D / 4);
+    window_reduce_kernel<D><<<(unsigned)ceil_div(quads, 256), 256, 0, st>>>(part, pieces, tile0, tiles, s->N, quads,
+                                                                           p.dK, p.dV);
+  }
+  return cuda_status(cudaGetLastError());
+}
+
 // ---------------------------------------------------------------- paged cache
 sparge_status check_cache(const sparge_cache* c, const sparge_cache_batch* b, CacheView* v) {
   if (c == nullptr || b == nullptr) return SPARGE_ERR_INVALID_ARG;
@@ -137,7 +210,7 @@ extern "C" {
 size_t sparge_window_workspace_bytes(int op, const sparge_window_shape* shape, const sparge_window* window) {
   WDims dm;
   if (check_window(shape, window, &dm) != SPARGE_OK) return 0;
-  return window_ws(op, dm);
+  return window_ws(op, shape, window, dm);
 }
 
 sparge_status sparge_window_fwd(const void* Q, const void* K, const void* V, const sparge_window_shape* shape,
@@ -147,7 +220,7 @@ sparge_status sparge_window_fwd(const void* Q, const void* K, const void* V, con
   sparge_status st = check_window(shape, window, &dm);
   if (st != SPARGE_OK) return st;
   if (!all_aligned16({Q, K, V, O})) return SPARGE_ERR_INVALID_ARG;
-  st = check_ws(workspace, workspace_bytes, window_ws(SPARGE_OP_WINDOW_FWD, dm));
+  st = check_ws(workspace, workspace_bytes, window_ws(SPARGE_OP_WINDOW_FWD, shape, window, dm));
   if (st != SPARGE_OK) return st;
   if (shape->d == 64) return launch_window_fwd<64>(Q, K, V, shape, window, lens, O, lse, dm, stream);
   return launch_window_fwd<128>(Q, K, V, shape, window, lens, O, lse, dm, stream);
@@ -161,26 +234,11 @@ sparge_status sparge_window_bwd(const void* Q, const void* K, const void* V, con
   sparge_status st = check_window(shape, window, &dm);
   if (st != SPARGE_OK) return st;
   if (!all_aligned16({Q, K, V, O, dO, dQ, dK, dV}) || !lse) return SPARGE_ERR_INVALID_ARG;
-  st = check_ws(workspace, workspace_bytes, window_ws(SPARGE_OP_WINDOW_BWD, dm));
+  st = check_ws(workspace, workspace_bytes, window_ws(SPARGE_OP_WINDOW_BWD, shape, window, dm));
   if (st != SPARGE_OK) return st;
-  WindowParams p = window_params(Q, K, V, shape, window, lens);
-  p.O_in = static_cast<const __nv_bfloat16*>(O);
-  p.dO = static_cast<const __nv_bfloat16*>(dO);
-  p.lse_in = lse;
-  p.dsum = static_cast<float*>(workspace);
-  p.dQ = static_cast<__nv_bfloat16*>(dQ);
-  p.dK = static_cast<__nv_bfloat16*>(dK);
-  p.dV = static_cast<__nv_bfloat16*>(dV);
-  const unsigned gq = (unsigned)ceil_div(dm.rows, 4), gk = (unsigned)ceil_div(dm.keys, 4);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (shape->d == 64) {
-    window_dq_simple<64><<<gq, 128, 0, s>>>(p, dm.rows);
-    window_dkdv_simple<64><<<gk, 128, 0, s>>>(p, dm.keys);
-  } else {
-    window_dq_simple<128><<<gq, 128, 0, s>>>(p, dm.rows);
-    window_dkdv_simple<128><<<gk, 128, 0, s>>>(p, dm.keys);
-  }
-  return cuda_status(cudaGetLastError());
+  if (shape->d == 64)
+    return launch_window_bwd<64>(Q, K, V, shape, window, lens, O, lse, dO, dQ, dK, dV, dm, workspace, stream);
+  return launch_window_bwd<128>(Q, K, V, shape, window, lens, O, lse, dO, dQ, dK, dV, dm, workspace, stream);
 }
 
 sparge_status sparge_cache_write(const sparge_cache* cache, const sparge_cache_batch* batch, const void* K,
