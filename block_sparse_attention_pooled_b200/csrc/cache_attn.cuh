@@ -1,63 +1,492 @@
-// Attention of new tokens over the paged cache.
+// Attention of few new tokens over the paged cache (one token of each of G
+// heads when decoding): bound by reading the cache once.
+//
+// Persistent CTAs with equal runs of 64-key tiles (cache_sched.cuh). A producer
+// warp fills a ring of K and V tiles by TMA through the page table (one box per
+// page and 64 columns; 128 bytes of swizzle); the other warps take whole tiles
+// in turn, each with a running maximum and sum and an accumulator of its own,
+// so that nothing but the ring orders them, and are joined in shared memory at
+// the end of an item. Scores are kept transposed (keys x rows): with at most 8
+// rows the 16-wide side of mma.m16n8k16 is the keys' and the channels', and a
+// tile costs half the instructions. P^T turns from accumulator to operand by
+// movmatrix, in registers.
+//   S^T = K Q^T (16 keys x 8 rows x 16 channels a step), O^T += V^T P^T.
+// e4m3: a lane takes 16 codes of a row at a time, which fixes the order of the
+// channels within a step (Q is read in the same order); a code becomes bf16 by
+// its bits (exponent and mantissa shifted into place, times 2^120), exactly;
+// K's power multiplies the scores, V's the probabilities.
 #pragma once
+#include <cuda.h>
 #include <cstdint>
 #include <cuda_bf16.h>
 
-#include "cache.cuh"
-#include "window.cuh"
+#include "cache_sched.cuh"
+#include "ptx.cuh"
 
 namespace sparge {
 
-struct CacheAttnParams {
-  CacheView c;
-  Window w;
-  const __nv_bfloat16* Q;
-  int64_t q_stride;
-  __nv_bfloat16* O;
-  float* lse;
-  int H;
-  float scale;
+enum : unsigned int { kErrCaFull = 0xB00, kErrCaEmpty, kErrCaDrain };
+
+constexpr int kDecKeys = 64;  // keys per tile
+
+template <int D, bool E4M3, int R8>
+struct DecSmem {
+  static constexpr int NW = E4M3 ? 8 : 4;                // consumer warps
+  static constexpr int kRows = 8 * R8;
+  static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
+  static constexpr int kTile = kDecKeys * kRowBytes;     // K or V
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kOStride = D + 4;                 // floats; + 4: the lanes' rows fall into different banks
+  static constexpr int kMerge = NW * kRows * (kOStride * 4 + 8);
+  static constexpr int kBudget = 225 * 1024 - kMerge - 2048;
+  static constexpr int NS = kBudget / (kStage + 160) > 16 ? 16 : kBudget / (kStage + 160);
+  static constexpr int kOffExp = NS * kStage;            // per stage: K's and V's powers, 64 bytes each
+  static constexpr int kOffMask = kOffExp + NS * 128;    // per stage: which 16-key groups exist
+  static constexpr int kOffBar = kOffMask + NS * 4 + (NS & 1) * 4;
+  static constexpr int kOffMl = kOffBar + 2 * NS * 8;
+  static constexpr int kOffO = (kOffMl + NW * kRows * 8 + 15) / 16 * 16;
+  static constexpr int kOffAbort = kOffO + NW * kRows * kOStride * 4;
+  static constexpr int kBytes = kOffAbort + 16 + 1024;
+  static constexpr int kThreads = (NW + 1) * 32;
+  static_assert(kBytes <= 227 * 1024);
 };
 
-// One warp per (token, head): lane l holds channels l, l + 32, ...
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(128) cache_attn_simple(const CacheAttnParams p) {
-  constexpr int C = D / 32;
-  const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32, h = (int)(row % p.H);
-  const int64_t t = row / p.H;
-  if (t >= min(__ldg(p.c.cu + p.c.B), p.c.tokens)) return;
-  const int b = find_seq(p.c.cu, p.c.B, (int)t);
-  const int c0 = __ldg(p.c.cu + b), first = __ldg(p.c.first + b);
-  const int L = first + __ldg(p.c.cu + b + 1) - c0, i = first + (int)t - c0;
-  const int hk = h / (p.H / p.c.Hkv);
-  float q[C], o[C] = {}, m = -INFINITY, l = 0.0f;
-#pragma unroll
-  for (int c = 0; c < C; ++c) q[c] = __bfloat162float(p.Q[t * p.q_stride + h * D + c * 32 + lane]);
-  const int lo = p.w.lo(i), hi = p.w.hi(i, L), ns = min(min(p.w.sinks, lo), hi);
-  for (int k = 0; k < ns + max(hi - lo, 0); ++k) {
-    int64_t at = cache_row(p.c, b, k < ns ? k : lo + k - ns);
-    if (at < 0) continue;
-    at += (int64_t)hk << p.c.page_shift;
-    auto val = [&](const uint8_t* x, const uint8_t* e, int c) -> float {
-      const int64_t a = at * D + c * 32 + lane;
-      if (!E4M3) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(x)[a]);
-      const __half_raw hr = __nv_cvt_fp8_to_halfraw(x[a], __NV_E4M3);
-      return __half2float(*reinterpret_cast<const __half*>(&hr)) * exp_scale(e[at]);
-    };
-    float s = 0.0f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) s += q[c] * val(p.c.k, p.c.k_exp, c);
-    s = warp_sum(s) * p.scale;
-    const float mn = fmaxf(m, s), f = __expf(m - mn), e = __expf(s - mn);
-    m = mn;
-    l = l * f + e;
-#pragma unroll
-    for (int c = 0; c < C; ++c) o[c] = o[c] * f + e * val(p.c.v, p.c.v_exp, c);
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// c += a b, 16 x 8 x 16.
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 codes in the upper bytes of u's halves -> bf16 pair, exact: sign,
+// exponent and mantissa in place make the value times 2^-120.
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t u) {
+  const uint32_t r = ((u & 0x7F007F00u) >> 4) | (u & 0x80008000u);
+  const uint32_t k = 0x7B807B80u;  // 2^120, twice
+  const __nv_bfloat162 v =
+      __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r), *reinterpret_cast<const __nv_bfloat162*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int D, bool E4M3, int R8>
+__global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
+    cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const CacheAttnParams p) {
+  using L = DecSmem<D, E4M3, R8>;
+  constexpr int NS = L::NS, NW = L::NW, KT = kDecKeys;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* sgen = smem_raw + (sbase - raw);
+  auto full = [&](int i) { return sbase + L::kOffBar + 8u * (uint32_t)i; };
+  auto empty = [&](int i) { return sbase + L::kOffBar + 8u * (uint32_t)(NS + i); };
+  uint32_t* masks = reinterpret_cast<uint32_t*>(sgen + L::kOffMask);
+  float2* wml = reinterpret_cast<float2*>(sgen + L::kOffMl);
+  float* wo = reinterpret_cast<float*>(sgen + L::kOffO);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + L::kOffAbort);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
   }
+  __syncthreads();
+  const int64_t W = count_units<KT>(p, lane);
+  const int ctas = ctas_used(W, p.ctas);
+  if ((int)blockIdx.x >= ctas) return;
+  const int64_t start = run_start(W, ctas, blockIdx.x), end = run_start(W, ctas, blockIdx.x + 1);
+  int at;
+  CacheItem<KT> it = find_unit<KT>(p, start, lane, at);
+  int64_t left = end - start;
+
+  if (warp == NW) {
+    // ------------------------------------------------------------ producer
+    const int box_shift = min(p.c.page_shift, 6), boxes = KT >> box_shift;  // keys per box: a page's, 64 at most
+    uint32_t n = 0;
+    bool ok = true;
+    while (ok && left > 0) {
+      const int stop = (int)min((int64_t)it.T, at + left);
+      left -= stop - at;
+      for (int t = at; t < stop; ++t, ++n) {
+        const int slot = n % NS;
+        const int pos = it.kt.key0(t) + (lane << box_shift);
+        const int64_t row = lane < boxes && pos < it.len() ? cache_row(p.c, it.b, pos) : -1;  // a page's row, head 0
+        ok = n < NS || role_wait(empty(slot), (n / NS - 1) & 1, kErrCaEmpty, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const unsigned there = __ballot_sync(0xffffffffu, row >= 0);
+        if (lane == 0) {
+          uint32_t m = 0;  // one bit per 16 keys
+          for (int x = 0; x < boxes; ++x)
+            if (there >> x & 1u) m |= ((1u << (1 << (box_shift - 4))) - 1u) << (x << (box_shift - 4));
+          masks[slot] = m;
+          const uint32_t bytes = (uint32_t)__popc(there) << box_shift;
+          mbar_arrive_expect_tx(full(slot), bytes * (2 * L::kRowBytes + (E4M3 ? 2 : 0)));
+        }
+        __syncwarp();
+        if (row >= 0) {
+          const uint32_t dst = sbase + slot * L::kStage + (lane << box_shift) * (E4M3 ? D : 128);
+          const int place = pos & ((1 << p.c.page_shift) - 1);
+          const int64_t head = row + ((int64_t)it.hk << p.c.page_shift);
+          const int z = (int)((head - place) >> p.c.page_shift);
+          if (E4M3) {
+            tma_load_3d(dst, &tmK, full(slot), 0, place, z);
+            tma_load_3d(dst + L::kTile, &tmV, full(slot), 0, place, z);
+            const uint32_t ex = sbase + L::kOffExp + slot * 128 + (lane << box_shift);
+            bulk_load(ex, p.c.k_exp + head, 1u << box_shift, full(slot));
+            bulk_load(ex + 64, p.c.v_exp + head, 1u << box_shift, full(slot));
+          } else {
 #pragma unroll
-  for (int c = 0; c < C; ++c) p.O[row * D + c * 32 + lane] = __float2bfloat16_rn(l > 0.0f ? o[c] / l : 0.0f);
-  if (p.lse && lane == 0) p.lse[row] = l > 0.0f ? m + logf(l) : -INFINITY;
+            for (int c = 0; c < D / 64; ++c) {
+              tma_load_3d(dst + c * (KT * 128), &tmK, full(slot), c * 64, place, z);
+              tma_load_3d(dst + c * (KT * 128) + L::kTile, &tmV, full(slot), c * 64, place, z);
+            }
+          }
+        }
+        __syncwarp();
+      }
+      if (left > 0 && !it.next(p)) break;
+      at = 0;
+    }
+    // Never leave with copies in flight.
+    if (lane == 0)
+      for (uint32_t i = n > NS ? n - NS : 0; i < n; ++i) mbar_wait(full(i % NS), (i / NS) & 1, kErrCaDrain);
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int g = lane >> 2, c = lane & 3;
+  uint32_t n = 0;
+  bool ok = true;
+  while (ok && left > 0) {
+    const int at0 = at, stop = (int)min((int64_t)it.T, at + left);
+    const int t0 = it.tile * p.tpt, tokens = min(p.tpt, it.n - t0), len = it.len();
+    const int64_t unit0 = end - left - at;  // the item's first unit
+    left -= stop - at;
+    // Q as operand B: rows 8 x + g, channels as the keys' operand has them.
+    uint32_t q[R8][D / 16][2];
+#pragma unroll
+    for (int x = 0; x < R8; ++x) {
+      const int r = 8 * x + g;
+      const bool live = r < tokens * p.G;
+      const __nv_bfloat16* src =
+          p.Q + (int64_t)(it.cu + t0 + (live ? r / p.G : 0)) * p.q_stride + (it.hk * p.G + (live ? r % p.G : 0)) * D;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        if (E4M3) {
+          const uint2 v = *reinterpret_cast<const uint2*>(src + 64 * (k / 4) + 16 * c + 4 * (k % 4));
+          q[x][k][0] = v.x;
+          q[x][k][1] = v.y;
+        } else {
+          q[x][k][0] = *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * c);
+          q[x][k][1] = *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * c + 8);
+        }
+      }
+    }
+    // The lane's rows in the accumulators: 8 x + 2 c + y.
+    int lo[R8][2], hi[R8][2];
+    float m_run[R8][2], l_run[R8][2], o[D / 16][R8][4];
+#pragma unroll
+    for (int x = 0; x < R8; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int i = it.first + t0 + min((8 * x + 2 * c + y) / p.G, tokens - 1);
+        lo[x][y] = p.w.lo(i);
+        hi[x][y] = p.w.hi(i, len);
+        m_run[x][y] = -INFINITY;
+        l_run[x][y] = 0.0f;
+      }
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int x = 0; x < R8; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) o[k][x][y] = 0.0f;
+    const int all_lo = p.w.lo(it.first + t0 + tokens - 1), all_hi = p.w.hi(it.first + t0, len);
+
+    for (int t = at; t < stop; ++t, ++n) {
+      if (n % NW != warp) continue;
+      const int slot = n % NS, key0 = it.kt.key0(t);
+      const bool sink = t < it.kt.ns;
+      ok = __all_sync(0xffffffffu, role_wait(full(slot), (n / NS) & 1, kErrCaFull, abort_flag));
+      if (!ok) break;
+      const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(masks + slot);
+      const uint32_t sk = sbase + slot * L::kStage, sv = sk + L::kTile, ex = sbase + L::kOffExp + slot * 128;
+      const bool exists = mask == 0xFu && key0 + KT <= len;
+      const bool whole = exists && (sink ? key0 + KT <= min(it.kt.cut, all_hi) : key0 >= all_lo && key0 + KT <= all_hi);
+      if (!E4M3 && !exists) {
+        // Zeros in V's rows that do not exist: memory may hold NaN there, and 0 * NaN is not 0.
+        for (int e = lane; e < KT * (D / 8); e += 32) {
+          const int r = e / (D / 8), ch = e % (D / 8);
+          if (key0 + r >= len || !(mask >> (r >> 4) & 1u))
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(sv + (ch / 8) * (KT * 128) + r * 128 +
+                                                                          (ch % 8) * 16),
+                         "r"(0)
+                         : "memory");
+        }
+        fence_async_smem();
+        __syncwarp();
+      }
+      // S^T
+      float s[KT / 16][R8][4];
+#pragma unroll
+      for (int mt = 0; mt < KT / 16; ++mt) {
+#pragma unroll
+        for (int x = 0; x < R8; ++x)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) s[mt][x][y] = 0.0f;
+        if (E4M3) {
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            uint32_t w[2][4];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int r = 16 * mt + g + 8 * y, ch = 4 * j + c;
+              const uint4 v = lds128(sk + r * D + (D == 128 ? (ch ^ (r & 7)) : (ch ^ ((r >> 1) & 3))) * 16);
+              w[y][0] = v.x, w[y][1] = v.y, w[y][2] = v.z, w[y][3] = v.w;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t a[4] = {
+                  codes_to_bf16(__byte_perm(w[0][k], 0, 0x1404)), codes_to_bf16(__byte_perm(w[1][k], 0, 0x1404)),
+                  codes_to_bf16(__byte_perm(w[0][k], 0, 0x3424)), codes_to_bf16(__byte_perm(w[1][k], 0, 0x3424))};
+#pragma unroll
+              for (int x = 0; x < R8; ++x) mma16816(s[mt][x], a, q[x][4 * j + k][0], q[x][4 * j + k][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const int r = 16 * mt + (lane & 15), ch = 2 * k + (lane >> 4);
+            uint32_t a[4];
+            ldsm4(sk + (ch / 8) * (KT * 128) + r * 128 + (((ch % 8) ^ (r & 7)) * 16), a);
+#pragma unroll
+            for (int x = 0; x < R8; ++x) mma16816(s[mt][x], a, q[x][k][0], q[x][k][1]);
+          }
+        }
+      }
+      // To log2 units; keys that a row does not see to -inf.
+      float pv[KT / 16][2];  // e4m3: V's powers of the lane's keys
+#pragma unroll
+      for (int mt = 0; mt < KT / 16; ++mt)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          float f = p.scale_log2;
+          if (E4M3) {
+            const int r = 16 * mt + g + 8 * z;
+            f *= exp_scale((uint8_t)lds_u8(ex + r));
+            pv[mt][z] = exp_scale((uint8_t)lds_u8(ex + 64 + r));
+          }
+#pragma unroll
+          for (int x = 0; x < R8; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) s[mt][x][2 * z + y] *= f;
+        }
+      if (!whole) {
+        const int most = sink ? it.kt.cut : len;
+#pragma unroll
+        for (int mt = 0; mt < KT / 16; ++mt)
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const int j = key0 + 16 * mt + g + 8 * z;
+            const bool here = (mask >> mt & 1u) && j < most;
+#pragma unroll
+            for (int x = 0; x < R8; ++x)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const bool seen = here & (j < hi[x][y]) & ((j >= lo[x][y]) | (j < p.w.sinks));
+                s[mt][x][2 * z + y] = seen ? s[mt][x][2 * z + y] : -INFINITY;
+              }
+          }
+      }
+      // Running maximum and sum; P^T as operand B, two 16-bit keys a register.
+      uint32_t b[KT / 16][R8][2];
+#pragma unroll
+      for (int x = 0; x < R8; ++x) {
+        float top[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float m = fmaxf(s[0][x][y], s[0][x][2 + y]);
+#pragma unroll
+          for (int mt = 1; mt < KT / 16; ++mt) m = fmax3(m, s[mt][x][y], s[mt][x][2 + y]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+          top[y] = fmaxf(m, m_run[x][y]);
+        }
+        if (__any_sync(0xffffffffu, top[0] > m_run[x][0] || top[1] > m_run[x][1])) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float f = top[y] == -INFINITY ? 1.0f : ex2_approx(m_run[x][y] - top[y]);
+            l_run[x][y] *= f;
+            m_run[x][y] = top[y];
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              o[k][x][y] *= f;
+              o[k][x][2 + y] *= f;
+            }
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float ref = m_run[x][y] == -INFINITY ? 0.0f : m_run[x][y];
+#pragma unroll
+          for (int mt = 0; mt < KT / 16; ++mt)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              float e = ex2_approx(s[mt][x][2 * z + y] - ref);
+              l_run[x][y] += e;
+              if (E4M3) e = e > 0.0f ? e * pv[mt][z] : 0.0f;  // a masked key's power may be anything
+              s[mt][x][2 * z + y] = e;
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < KT / 16; ++mt) {
+          b[mt][x][0] = movmatrix_t(pack_bf16x2(s[mt][x][0], s[mt][x][1]));
+          b[mt][x][1] = movmatrix_t(pack_bf16x2(s[mt][x][2], s[mt][x][3]));
+        }
+      }
+      // O^T
+#pragma unroll
+      for (int mt = 0; mt < KT / 16; ++mt) {
+        if (E4M3) {
+          constexpr int NB = D / 8;  // codes per lane and key row
+          uint32_t w[4][NB / 4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int r = 16 * mt + 2 * c + (y & 1) + 8 * (y >> 1);
+            if (D == 128) {
+              const uint4 v = lds128(sv + r * D + ((g ^ (r & 7)) * 16));
+              w[y][0] = v.x, w[y][1] = v.y, w[y][NB / 4 - 2] = v.z, w[y][NB / 4 - 1] = v.w;
+            } else {
+              const uint2 v = lds64(sv + r * D + (((g >> 1) ^ ((r >> 1) & 3)) * 16) + (g & 1) * 8);
+              w[y][0] = v.x, w[y][1] = v.y;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {  // rows g and g + 8 of step k: channels NB g + 2 k and + 1
+            const int i = k / 2, h = (k & 1) * 2;
+            uint32_t a[4];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              // byte h (then h + 1) of both keys' words, into the halves' upper bytes
+              const uint32_t u = __byte_perm(w[2 * y][i], w[2 * y + 1][i], h == 0 ? 0x4000 : 0x6020);
+              const uint32_t v = __byte_perm(w[2 * y][i], w[2 * y + 1][i], h == 0 ? 0x5010 : 0x7030);
+              a[2 * y] = codes_to_bf16(u);
+              a[2 * y + 1] = codes_to_bf16(v);
+            }
+#pragma unroll
+            for (int x = 0; x < R8; ++x) mma16816(o[k][x], a, b[mt][x][0], b[mt][x][1]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const int r = 16 * mt + (lane & 7) + 8 * (lane >> 4), ch = 2 * k + ((lane >> 3) & 1);
+            uint32_t a[4];
+            ldsm4_t(sv + (ch / 8) * (KT * 128) + r * 128 + (((ch % 8) ^ (r & 7)) * 16), a);
+#pragma unroll
+            for (int x = 0; x < R8; ++x) mma16816(o[k][x], a, b[mt][x][0], b[mt][x][1]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(slot));
+    }
+    // Join the warps.
+#pragma unroll
+    for (int x = 0; x < R8; ++x)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l_run[x][y] += __shfl_xor_sync(0xffffffffu, l_run[x][y], d);
+        const int r = 8 * x + 2 * c + y;
+        if (g == 0) wml[warp * L::kRows + r] = make_float2(m_run[x][y], l_run[x][y]);
+        float* dst = wo + (warp * L::kRows + r) * L::kOStride;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const int ch = E4M3 ? (D / 8) * g + 2 * k : 16 * k + g, ch2 = E4M3 ? ch + 1 : ch + 8;
+          dst[ch] = o[k][x][y];
+          dst[ch2] = o[k][x][2 + y];
+        }
+      }
+    asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory");
+    const bool all = at0 == 0 && stop == it.T;
+    const int64_t slot0 = (int64_t)(2 * blockIdx.x + (start < unit0 ? 1 : 0)) * L::kRows;
+    constexpr int TPR = D / 4;  // threads per row, four channels each
+    for (int r = threadIdx.x / TPR; r < tokens * p.G; r += NW * 32 / TPR) {
+      const int ch = (threadIdx.x % TPR) * 4;
+      float m = -INFINITY, l = 0.0f;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) m = fmaxf(m, wml[w * L::kRows + r].x);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float2 ml = wml[w * L::kRows + r];
+        const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
+        const float4 v = *reinterpret_cast<const float4*>(wo + (w * L::kRows + r) * L::kOStride + ch);
+        l += ml.y * f;
+        acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
+      }
+      if (all) {
+        const int64_t row = (int64_t)(it.cu + t0 + r / p.G) * p.H + it.hk * p.G + r % p.G;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        *reinterpret_cast<uint2*>(p.O + row * D + ch) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (p.lse && ch == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+      } else {
+        *reinterpret_cast<float4*>(p.part_o + (slot0 + r) * D + ch) = acc;
+        if (ch == 0) p.part_ml[slot0 + r] = make_float2(m, l);
+      }
+    }
+    // All leave together if one gave up.
+    int gone;
+    asm volatile(
+        "{\n\t.reg .pred q, r;\n\tsetp.ne.b32 q, %1, 0;\n\tbarrier.cta.red.or.pred r, 1, %2, q;\n\t"
+        "selp.b32 %0, 1, 0, r;\n\t}"
+        : "=r"(gone)
+        : "r"((int)(!ok || *abort_flag)), "n"(NW * 32)
+        : "memory");
+    if (gone || (left > 0 && !it.next(p))) break;
+    at = 0;
+  }
 }
 
 }  // namespace sparge

@@ -1,0 +1,374 @@
+// Attention of a chunk of new tokens over the paged cache on the 5th-generation
+// tensor cores: window_fwd_kernel's structure (two 128-row tiles that alternate
+// between the tensor core and their softmax) over the equal runs of key tiles
+// of cache_sched.cuh.
+//
+// A row is a (token, head of the K/V head's group) pair, token by token, so a
+// tile holds 128 / G tokens and K and V are read once for the whole group. The
+// rows of Q come by a 4-D TMA box {64 channels, G heads, 128 / G tokens}.
+// K and V, bf16: by TMA, one box per page; a tile with places that do not exist
+// is copied by the producer's lanes, zeros there. e4m3: four more warps load
+// the codes (the next tile's while they convert this one's) and write them into
+// the ring as bf16, each times its row's power: exact.
+#pragma once
+#include <cuda.h>
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "cache_attn.cuh"
+#include "cache_sched.cuh"
+#include "wattn.cuh"
+
+namespace sparge {
+
+enum : unsigned int {
+  kErrCcQ = 0xC00, kErrCcQEmpty, kErrCcKvFull, kErrCcKvEmpty, kErrCcS, kErrCcP, kErrCcO, kErrCcOFree, kErrCcDrain
+};
+
+template <bool E4M3>
+__host__ __device__ constexpr int chunk_threads() { return E4M3 ? 512 : 384; }
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
+    cache_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const CacheAttnParams p) {
+  using L = WSmem<D>;
+  constexpr int NS = L::NS, KT = kWTile;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* sgen = smem_raw + (sbase - raw);
+  const uint32_t sQ = sbase + L::kOffQ, sKv = sbase + L::kOffKv;
+  auto bar = [&](int i) { return sbase + L::kOffBar + 8u * (uint32_t)i; };
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sgen + L::kOffTmem);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + L::kOffTmem + 4);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kNumBars; ++i) {
+      const bool rows = (i >= L::kBarP && i < L::kBarP + 2) || (i >= L::kBarOFree && i < L::kBarOFree + 2);
+      const bool conv = E4M3 && i >= L::kBarKvFull && i < L::kBarKvFull + NS;
+      mbar_init(bar(i), rows || conv ? 128 : 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(sbase + L::kOffTmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int tq = p.tpt / 2;  // tokens per 128-row tile
+
+  // This CTA's run of units.
+  const int64_t W = count_units<KT>(p, lane);
+  const int ctas = ctas_used(W, p.ctas);
+  const bool work = (int)blockIdx.x < ctas;
+  const int64_t start = work ? run_start(W, ctas, blockIdx.x) : 0, end = work ? run_start(W, ctas, blockIdx.x + 1) : 0;
+  int at = 0;
+  CacheItem<KT> it;
+  if (work) it = find_unit<KT>(p, start, lane, at);
+  int64_t left = end - start;
+  auto few_registers = [] {
+    if (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  };
+  // Ends a piece of an item; false when the run is done.
+  auto advance = [&](int stop) {
+    left -= stop - at;
+    at = 0;
+    return left > 0 && it.next(p);
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    few_registers();
+    uint32_t n = 0, nq = 0;
+    bool ok = true;
+    if (work) do {
+      const int stop = (int)min((int64_t)it.T, at + left);
+      ok = nq == 0 || role_wait(bar(L::kBarQEmpty), (nq - 1) & 1, kErrCcQEmpty, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(L::kBarQFull), 2 * (D / 64) * tq * p.G * 128);
+        for (int h = 0; h < 2; ++h)
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(sQ + h * L::kTileBytes + c * (kWTile * 128), &tmQ, bar(L::kBarQFull), c * 64, 0,
+                        it.cu + it.tile * p.tpt + h * tq, it.hk);
+      }
+      ++nq;
+      if (!E4M3) {
+        const int box_shift = min(p.c.page_shift, 6), boxes = KT >> box_shift, len = it.len();
+        for (int t = 2 * at; ok && t < 2 * stop; ++t, ++n) {  // K(0), V(0), K(1), V(1), ...
+          const int slot = n % NS, key0 = it.kt.key0(t >> 1);
+          const int pos = key0 + (lane << box_shift);
+          const int64_t row = lane < boxes && pos < len ? cache_row(p.c, it.b, pos) : -1;
+          ok = n < NS || role_wait(bar(L::kBarKvEmpty + slot), (n / NS - 1) & 1, kErrCcKvEmpty, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t dst = sKv + slot * L::kTileBytes;
+          const unsigned there = __ballot_sync(0xffffffffu, row >= 0);
+          if (key0 + KT > len || __popc(there) < boxes) {
+            const __nv_bfloat16* base = reinterpret_cast<const __nv_bfloat16*>((t & 1) ? p.c.v : p.c.k);
+            copy_tile<D>(dst, lane, [&](int r) -> const __nv_bfloat16* {
+              const int64_t x = key0 + r < len ? cache_row(p.c, it.b, key0 + r) : -1;
+              return x < 0 ? nullptr : base + (x + ((int64_t)it.hk << p.c.page_shift)) * D;
+            });
+            if (lane == 0) mbar_arrive(bar(L::kBarKvFull + slot));
+          } else {
+            if (lane == 0) mbar_arrive_expect_tx(bar(L::kBarKvFull + slot), L::kTileBytes);
+            __syncwarp();
+            if (lane < boxes) {
+              const int place = pos & ((1 << p.c.page_shift) - 1);
+              const int z = (int)((row - place + ((int64_t)it.hk << p.c.page_shift)) >> p.c.page_shift);
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_3d(dst + c * (KT * 128) + (lane << box_shift) * 128, (t & 1) ? &tmV : &tmK,
+                            bar(L::kBarKvFull + slot), c * 64, place, z);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok || !advance(stop)) break;
+    } while (true);
+    // Never leave with copies in flight.
+    if (lane == 0) {
+      if (nq) mbar_wait(bar(L::kBarQFull), (nq - 1) & 1, kErrCcQ);
+      if (!E4M3)
+        for (uint32_t i = n > NS ? n - NS : 0; i < n; ++i)
+          mbar_wait(bar(L::kBarKvFull + i % NS), (i / NS) & 1, kErrCcKvFull);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    few_registers();
+    const bool leader = elect_one();
+    constexpr uint32_t idS = idesc_bf16_f32(kWTile, kWTile, false, false);
+    constexpr uint32_t idO = idesc_bf16_f32(kWTile, D, false, true);
+    const uint64_t dQ = sdesc_sw128(sQ, 16, 1024);
+    const uint64_t dKm = sdesc_sw128(sKv, 16, 1024);
+    const uint64_t dVm = sdesc_sw128(sKv, kWTile * 128, 1024);
+    auto wait = [&](int b, uint32_t parity, unsigned int site) {
+      return __all_sync(0xffffffffu, role_wait(bar(b), parity, site, abort_flag));
+    };
+    uint32_t n = 0, nq = 0, np = 0;
+    bool ok = true;
+    auto issue_s = [&](int x, int slot) {
+      if (leader) {
+        const uint64_t q = dQ + (uint64_t)((x * L::kTileBytes) >> 4), k = dKm + (uint64_t)((slot * L::kTileBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = ((kk >> 2) * (kWTile * 128) + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + x * 128, q + o, k + o, idS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(bar(L::kBarS + x));
+      }
+      __syncwarp();
+    };
+    if (work) do {
+      const int stop = (int)min((int64_t)it.T, at + left), total = stop - at;
+      ok = wait(L::kBarQFull, nq & 1, kErrCcQ) && wait(L::kBarKvFull + n % NS, (n / NS) & 1, kErrCcKvFull);
+      if (!ok) break;
+      tc_fence_after();
+      issue_s(0, n % NS);
+      issue_s(1, n % NS);
+      if (leader) {
+        mma_commit(bar(L::kBarKvEmpty + n % NS));
+        if (total == 1) mma_commit(bar(L::kBarQEmpty));
+      }
+      __syncwarp();
+      ++n;
+      for (int t = 0; ok && t < total; ++t, ++np) {
+        const int vs = n % NS, ks = (n + 1) % NS;
+        const bool more = t + 1 < total;
+        for (int x = 0; x < 2; ++x) {
+          if (x == 0) ok = wait(L::kBarKvFull + vs, (n / NS) & 1, kErrCcKvFull);
+          if (ok && t == 0 && nq > 0) ok = wait(L::kBarOFree + x, (nq - 1) & 1, kErrCcOFree);
+          ok = ok && wait(L::kBarP + x, np & 1, kErrCcP);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t v = dVm + (uint64_t)((vs * L::kTileBytes) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kWTile / 16; ++kk)
+              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, v + kk * 128, idO, (t > 0 || kk > 0) ? 1u : 0u);
+            if (x == 1) mma_commit(bar(L::kBarKvEmpty + vs));
+            if (!more) mma_commit(bar(L::kBarO + x));
+          }
+          __syncwarp();
+          if (more) {
+            if (x == 0) ok = wait(L::kBarKvFull + ks, ((n + 1) / NS) & 1, kErrCcKvFull);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(x, ks);
+            if (x == 1 && leader) {
+              mma_commit(bar(L::kBarKvEmpty + ks));
+              if (t + 2 == total) mma_commit(bar(L::kBarQEmpty));
+            }
+            __syncwarp();
+          }
+        }
+        n += more ? 2 : 1;
+      }
+      ++nq;
+      if (!ok || !advance(stop)) break;
+    } while (true);
+    if (leader) mma_commit(bar(L::kBarDrain));
+    __syncwarp();
+    mbar_wait(bar(L::kBarDrain), 0, kErrCcDrain);
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------------------------ softmax and epilogue
+    if (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int x = (warp - 4) / 4;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + x * 128 + lane_off, to = tmem + 256 + x * 128 + lane_off;
+    uint32_t nq = 0, np = 0;
+    bool ok = true;
+    if (work) do {
+      const int at0 = at, stop = (int)min((int64_t)it.T, at + left), len = it.len();
+      const int64_t unit0 = end - left - at;
+      const int tok = it.tile * p.tpt + x * tq + r / p.G;
+      const bool live = r < tq * p.G && tok < it.n;
+      const int i = it.first + min(tok, it.n - 1);
+      const int lo = p.w.lo(i), hi = p.w.hi(i, len);
+      const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
+      float m_run = -INFINITY, l_run = 0.0f;
+      for (int t = at; t < stop; ++t, ++np) {
+        const int key0 = it.kt.key0(t);
+        // Keys of pages that do not exist.
+        uint32_t gone[4] = {0, 0, 0, 0};
+        if (t < it.kt.total || it.kt.total == 0) {
+          const int g16 = key0 + lane * 16;
+          const bool absent = lane < 8 && g16 < len && cache_row(p.c, it.b, g16) < 0;
+          const unsigned m = __ballot_sync(0xffffffffu, absent);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            gone[c] = ((m >> (2 * c)) & 1u ? 0xFFFFu : 0u) | ((m >> (2 * c + 1)) & 1u ? 0xFFFF0000u : 0u);
+        }
+        ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarS + x), np & 1, kErrCcS, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        const bool sink = t < it.kt.ns;
+        const bool whole = (gone[0] | gone[1] | gone[2] | gone[3]) == 0 &&
+                           (sink ? key0 + KT <= min(it.kt.cut, all_hi) : key0 >= all_lo && key0 + KT <= all_hi);
+        const int e = (sink ? min(hi, it.kt.cut) : hi) - key0;
+        softmax_tile<D>(ts, to, t == at, whole, sink ? 0 : lo - key0, e, p.w.sinks - key0, p.scale_log2, m_run, l_run,
+                        gone);
+        tc_fence_before();
+        mbar_arrive(bar(L::kBarP + x));
+      }
+      if (!ok) break;
+      ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarO + x), nq & 1, kErrCcO, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      ++nq;
+      const int64_t row = (int64_t)(it.cu + tok) * p.H + it.hk * p.G + r % p.G;
+      const bool none = l_run == 0.0f;
+      if (at0 == 0 && stop == it.T) {
+        store_row<D>(p.O + row * D, to, none ? 0.0f : 1.0f / l_run, none, live);
+        if (live && p.lse) p.lse[row] = none ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
+      } else {
+        const int64_t slot = (int64_t)(2 * blockIdx.x + (start < unit0 ? 1 : 0)) * (2 * kWTile) + (x * tq * p.G + r);
+        float* out = p.part_o + slot * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(to + c, o);
+          tmem_ld_wait();
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4*>(out + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          }
+        }
+        if (live) p.part_ml[slot] = make_float2(m_run, l_run);
+      }
+      tc_fence_before();
+      mbar_arrive(bar(L::kBarOFree + x));
+      if (!advance(stop)) break;
+    } while (true);
+  } else if (E4M3 && warp >= 12) {
+    // ------------------------------------------------------------ codes to bf16
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    constexpr int CH = D / 16;             // 16-code pieces per row
+    constexpr int N = kWTile * CH / 128;   // pieces per thread and tile
+    const int tid = threadIdx.x - 384, c = tid % CH, r0 = tid / CH;
+    constexpr int RS = 128 / CH;           // rows between a thread's pieces
+    uint32_t n = 0;
+    bool ok = true;
+    uint4 code[N];
+    uint32_t power[N];  // bf16 2^e twice; 0 where the place does not exist
+    auto fetch = [&](int t) {
+      const int key0 = it.kt.key0(t >> 1), len = it.len();
+      const uint8_t *src = (t & 1) ? p.c.v : p.c.k, *ex = (t & 1) ? p.c.v_exp : p.c.k_exp;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int j = key0 + r0 + k * RS;
+        int64_t row = j < len ? cache_row(p.c, it.b, j) : -1;
+        code[k] = make_uint4(0, 0, 0, 0);
+        power[k] = 0;
+        if (row >= 0) {
+          row += (int64_t)it.hk << p.c.page_shift;
+          code[k] = *reinterpret_cast<const uint4*>(src + row * D + c * 16);
+          const uint32_t e = __ldg(ex + row);
+          power[k] = (e == 255 ? 0x7FC0u : e << 7) * 0x10001u;
+        }
+      }
+    };
+    if (work) {
+      int stop = (int)min((int64_t)it.T, at + left), t = 2 * at;
+      fetch(t);
+      while (true) {
+        const int slot = n % NS;
+        ok = n < NS || role_wait(bar(L::kBarKvEmpty + slot), (n / NS - 1) & 1, kErrCcKvEmpty, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t dst = sKv + slot * L::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const int r = r0 + k * RS;
+          const uint32_t w[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
+          const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&power[k]);
+          uint32_t v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t y = codes_to_bf16(__byte_perm(w[j / 2], 0, j & 1 ? 0x3424 : 0x1404));
+            const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), f);
+            v[j] = *reinterpret_cast<const uint32_t*>(&z);
+          }
+          const uint32_t line = dst + (2 * c / 8) * (kWTile * 128) + r * 128;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + ((((2 * c) % 8 + h) ^ (r & 7)) * 16)),
+                         "r"(v[4 * h]), "r"(v[4 * h + 1]), "r"(v[4 * h + 2]), "r"(v[4 * h + 3])
+                         : "memory");
+        }
+        fence_async_smem();
+        mbar_arrive(bar(L::kBarKvFull + slot));
+        ++n;
+        if (++t == 2 * stop) {
+          if (!advance(stop)) break;
+          stop = (int)min((int64_t)it.T, at + left);
+          t = 2 * at;
+        }
+        fetch(t);
+      }
+    }
+  } else {
+    few_registers();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace sparge

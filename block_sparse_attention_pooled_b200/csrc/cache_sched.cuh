@@ -1,0 +1,244 @@
+// How the work of attention over the paged cache is cut up. All lengths are in
+// device memory, so the kernels find their shares themselves.
+//
+// An item is a row tile (up to `tpt` consecutive new tokens of a sequence,
+// times the G heads that share a K/V head) of one K/V head; its units are the
+// key tiles of KT keys that any of its rows may see. The units of all items in
+// order (sequence, row tile, K/V head) are dealt to the CTAs in equal
+// contiguous runs: every CTA gets the same number of key tiles (to one),
+// however ragged the batch is. A run that ends inside an item leaves a partial
+// result; cache_combine_kernel joins an item's partials.
+#pragma once
+#include <cstdint>
+
+#include "cache.cuh"
+#include "window.cuh"
+
+namespace sparge {
+
+// The key tiles of a run of rows: `ns` tiles from key 0 that hold the sinks
+// below `lo`, then tiles from `lo` on. A sink tile's keys at or past `cut` are
+// not its own: they belong to the window's tiles or to nobody.
+template <int KT>
+struct KeyTilesT {
+  int ns, total, lo, cut;
+  __device__ __forceinline__ int key0(int t) const { return t < ns ? t * KT : lo + (t - ns) * KT; }
+};
+
+// lo: the first row's first key, rounded down by align_mask; hi: the last row's end.
+template <int KT>
+__device__ __forceinline__ KeyTilesT<KT> key_tiles_of(int lo, int hi, int sinks, int align_mask) {
+  KeyTilesT<KT> k;
+  k.lo = lo & ~align_mask;
+  k.cut = min(min(sinks, hi), k.lo);
+  k.ns = (k.cut + KT - 1) / KT;
+  if (k.ns * KT >= k.lo) k.lo = k.cut = k.ns = 0;  // the sinks' tiles reach the window: one run of tiles
+  k.total = k.ns + (max(hi - k.lo, 0) + KT - 1) / KT;
+  return k;
+}
+
+struct CacheAttnParams {
+  CacheView c;
+  Window w;
+  const __nv_bfloat16* Q;
+  int64_t q_stride;
+  __nv_bfloat16* O;
+  float* lse;
+  float* part_o;    // [2 * CTAs][rows][D]: a CTA's first and last partial
+  float2* part_ml;  // [2 * CTAs][rows]: reference (log2) and sum
+  int H, G;
+  int tpt;          // tokens per row tile
+  int ctas;         // CTAs that the units are dealt to
+  float scale_log2;
+};
+
+// One item and where its units lie. Held alike by all lanes of a warp.
+template <int KT>
+struct CacheItem {
+  int b, tile, hk;      // sequence, row tile, K/V head
+  int n, first, cu;     // the sequence's new tokens, its position, its first packed token
+  KeyTilesT<KT> kt;
+  int T;                // key tiles, at least 1
+
+  __device__ __forceinline__ void seq(const CacheAttnParams& p, int seq) {
+    b = seq;
+    const int end = min(__ldg(p.c.cu + b + 1), p.c.tokens);
+    cu = __ldg(p.c.cu + b);
+    n = max(end - cu, 0);
+    first = max(__ldg(p.c.first + b), 0);
+  }
+  __device__ __forceinline__ int len() const { return first + n; }
+  __device__ __forceinline__ void keys(const CacheAttnParams& p) {
+    const int t0 = tile * p.tpt, t1 = min(n, t0 + p.tpt) - 1;
+    kt = key_tiles_of<KT>(p.w.lo(first + t0), p.w.hi(first + t1, len()), p.w.sinks, (1 << p.c.page_shift) - 1);
+    T = max(kt.total, 1);
+  }
+  // To the next item; false past the last.
+  __device__ __forceinline__ bool next(const CacheAttnParams& p) {
+    if (++hk < p.c.Hkv) return true;
+    hk = 0;
+    if ((tile + 1) * p.tpt < n) {
+      ++tile;
+      keys(p);
+      return true;
+    }
+    tile = 0;
+    do {
+      if (b + 1 >= p.c.B) return false;
+      seq(p, b + 1);
+    } while (n == 0);
+    keys(p);
+    return true;
+  }
+};
+
+// Walks all (sequence, row tile) pairs, 32 at a time, and calls
+// f(b, tile, units of one K/V head) on the lanes that hold one; f returns true
+// to stop the walk. Called by a whole warp.
+template <int KT, typename F>
+__device__ __forceinline__ void walk_tiles(const CacheAttnParams& p, int lane, F f) {
+  for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+    CacheItem<KT> it;
+    int tiles = 0;
+    it.n = it.first = it.cu = 0;
+    if (b0 + lane < p.c.B) {
+      it.seq(p, b0 + lane);
+      tiles = (it.n + p.tpt - 1) / p.tpt;
+    }
+    int sum = tiles;  // inclusive prefix over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const int all = __shfl_sync(0xffffffffu, sum, 31);
+    for (int q0 = 0; q0 < all; q0 += 32) {
+      const int q = q0 + lane;
+      int src = 0;  // the lane whose sequence holds pair q: the first with sum > q
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const int v = __shfl_sync(0xffffffffu, sum, min(src + o - 1, 31));
+        if (v <= q) src += o;
+      }
+      src = min(src, 31);
+      CacheItem<KT> x;
+      x.b = b0 + src;
+      x.n = __shfl_sync(0xffffffffu, it.n, src);
+      x.first = __shfl_sync(0xffffffffu, it.first, src);
+      x.cu = __shfl_sync(0xffffffffu, it.cu, src);
+      x.tile = q - (__shfl_sync(0xffffffffu, sum, src) - __shfl_sync(0xffffffffu, tiles, src));
+      x.hk = 0;
+      x.T = 0;
+      if (q < all) x.keys(p);
+      if (f(x)) return;
+    }
+  }
+}
+
+// Units of all items.
+template <int KT>
+__device__ __forceinline__ int64_t count_units(const CacheAttnParams& p, int lane) {
+  int64_t total = 0;
+  walk_tiles<KT>(p, lane, [&](const CacheItem<KT>& x) {
+    total += x.T;
+    return false;
+  });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  return total * p.c.Hkv;
+}
+
+// The item that holds unit u (u < count_units) and u's place in it. Called by a whole warp.
+template <int KT>
+__device__ __forceinline__ CacheItem<KT> find_unit(const CacheAttnParams& p, int64_t u, int lane, int& at) {
+  int64_t base = 0;
+  CacheItem<KT> found;
+  walk_tiles<KT>(p, lane, [&](const CacheItem<KT>& x) {
+    int64_t sum = (int64_t)x.T * p.c.Hkv;
+    const int64_t own = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, base + sum > u);
+    if (past == 0) {
+      base += __shfl_sync(0xffffffffu, sum, 31);
+      return false;
+    }
+    const int src = __ffs(past) - 1;
+    found.b = __shfl_sync(0xffffffffu, x.b, src);
+    found.tile = __shfl_sync(0xffffffffu, x.tile, src);
+    found.n = __shfl_sync(0xffffffffu, x.n, src);
+    found.first = __shfl_sync(0xffffffffu, x.first, src);
+    found.cu = __shfl_sync(0xffffffffu, x.cu, src);
+    base += __shfl_sync(0xffffffffu, sum - own, src);
+    return true;
+  });
+  found.keys(p);
+  found.hk = (int)((u - base) / found.T);
+  at = (int)((u - base) % found.T);
+  return found;
+}
+
+// CTAs that get a run: two units at least, so that a short cache does not end
+// up in more partials than tiles.
+__device__ __forceinline__ int ctas_used(int64_t W, int ctas) { return (int)max((int64_t)1, min((int64_t)ctas, W / 2)); }
+
+// CTA c's units: [c W / ctas, (c + 1) W / ctas).
+__device__ __forceinline__ int64_t run_start(int64_t W, int ctas, int c) { return W * c / ctas; }
+
+// One warp per (packed token, K/V head): joins the partials of the item that
+// the token's rows lie in, if any, head by head. ROWS: rows of a partial.
+template <int D, int KT>
+__global__ void __launch_bounds__(128) cache_combine_kernel(const CacheAttnParams p, int rows) {
+  constexpr int C = D / 32;
+  const int lane = threadIdx.x % 32;
+  const int64_t id = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+  const int t = (int)(id / p.c.Hkv), hk = (int)(id % p.c.Hkv);
+  if (t >= min(__ldg(p.c.cu + p.c.B), p.c.tokens)) return;
+  const int64_t W = count_units<KT>(p, lane);
+  const int ctas = ctas_used(W, p.ctas);
+  // The units before the token's item.
+  const int b = find_seq(p.c.cu, p.c.B, t);
+  const int place = t - __ldg(p.c.cu + b), tile = place / p.tpt;
+  int64_t u0 = 0;
+  int T = 0;
+  walk_tiles<KT>(p, lane, [&](const CacheItem<KT>& x) {
+    const bool before = x.T > 0 && (x.b < b || (x.b == b && x.tile < tile));
+    if (before) u0 += x.T;
+    const unsigned here = __ballot_sync(0xffffffffu, x.T > 0 && x.b == b && x.tile == tile);
+    if (here) T = __shfl_sync(0xffffffffu, x.T, __ffs(here) - 1);
+    return here != 0;
+  });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) u0 += __shfl_xor_sync(0xffffffffu, u0, o);
+  u0 = u0 * p.c.Hkv + (int64_t)hk * T;
+  const int c0 = (int)(((u0 + 1) * ctas - 1) / W), c1 = (int)(((u0 + T) * ctas - 1) / W);  // owners of the ends
+  if (c0 == c1) return;  // one CTA did it all
+  for (int g = 0; g < p.G; ++g) {
+    const int r = (place - tile * p.tpt) * p.G + g;
+    // A CTA's partial is its last one if the item starts in it, else its first.
+    auto slot = [&](int c) { return (int64_t)(2 * c + (run_start(W, ctas, c) < u0 ? 1 : 0)) * rows + r; };
+    float m = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[slot(c)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.0f, o[C] = {};
+    for (int c = c0; c <= c1; ++c) {
+      const int64_t s = slot(c);
+      const float2 ml = p.part_ml[s];
+      if (!(ml.y > 0.0f) && ml.y == ml.y) continue;  // saw nothing
+      const float f = exp2f(ml.x - m);
+      l += ml.y * f;
+#pragma unroll
+      for (int k = 0; k < C; ++k) o[k] += p.part_o[s * D + k * 32 + lane] * f;
+    }
+    const int64_t row = (int64_t)t * p.H + hk * p.G + g;
+#pragma unroll
+    for (int k = 0; k < C; ++k) p.O[row * D + k * 32 + lane] = __float2bfloat16_rn(l == 0.0f ? 0.0f : o[k] / l);
+    if (p.lse && lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+}  // namespace sparge

@@ -24,9 +24,11 @@
 #include "selftest.cuh"
 #include "window.cuh"
 #include "cache.cuh"
+#include "cache_sched.cuh"
 #include "cache_attn.cuh"
 #include "wattn.cuh"
 #include "wattn_bwd.cuh"
+#include "cache_chunk.cuh"
 
 namespace {
 
@@ -138,12 +140,12 @@ bool make_map_bhnd(CUtensorMap* m, const void* base, int64_t BH, int N, int d, i
 // a thread asking for less cannot lower a limit another thread relies on.
 template <typename K>
 cudaError_t ensure_smem(K kernel, int bytes, int slot) {
-  static std::atomic<int> done[64][32];  // [device][slot]: one slot per kernel
+  static std::atomic<int> done[64][64];  // [device][slot]: one slot per kernel
   static std::mutex mu;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || slot < 0 || slot >= 32)
+  if (dev < 0 || dev >= 64 || slot < 0 || slot >= 64)
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (done[dev][slot].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
   std::lock_guard<std::mutex> lock(mu);

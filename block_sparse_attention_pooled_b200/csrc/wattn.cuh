@@ -28,7 +28,7 @@
 #include <cuda_bf16.h>
 
 #include "attn.cuh"
-#include "cache.cuh"
+#include "cache_sched.cuh"
 #include "ptx.cuh"
 #include "window.cuh"
 
@@ -94,23 +94,10 @@ __device__ __forceinline__ void copy_tile(uint32_t dst, int lane, Src src) {
   __syncwarp();
 }
 
-// The key tiles of a work item: `ns` tiles from key 0 that hold the sinks
-// below `lo`, then tiles from `lo` on. A sink tile's keys at or past `cut` are
-// not its own: they belong to the window's tiles or to nobody.
-struct KeyTiles {
-  int ns, total, lo, cut;
-  __device__ __forceinline__ int key0(int t) const { return t < ns ? t * kWTile : lo + (t - ns) * kWTile; }
-};
+using KeyTiles = KeyTilesT<kWTile>;
 
-// lo: the first row's first key, rounded down to `align`; hi: the last row's end.
 __device__ __forceinline__ KeyTiles key_tiles(int lo, int hi, int sinks, int align_mask) {
-  KeyTiles k;
-  k.lo = lo & ~align_mask;
-  k.cut = min(min(sinks, hi), k.lo);
-  k.ns = (k.cut + kWTile - 1) / kWTile;
-  if (k.ns * kWTile >= k.lo) k.lo = k.cut = k.ns = 0;  // the sinks' tiles reach the window: one run of tiles
-  k.total = k.ns + (max(hi - k.lo, 0) + kWTile - 1) / kWTile;
-  return k;
+  return key_tiles_of<kWTile>(lo, hi, sinks, align_mask);
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
@@ -121,6 +108,25 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
   for (int j = 0; j < 32; ++j) r[j] = __uint_as_float(v[j / 16][j % 16]);
 }
 
+// A row of D accumulator columns times f, as bf16.
+template <int D>
+__device__ __forceinline__ void store_row(__nv_bfloat16* out, uint32_t taddr, float f, bool zero, bool store) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    float o[32];
+    tmem_ld32(taddr + c, o);
+    tmem_ld_wait();
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = zero ? 0u : pack_bf16x2(o[2 * j] * f, o[2 * j + 1] * f);
+    if (store) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(out + c + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    }
+  }
+}
+
 // Bits 0 .. n - 1 (n at most 0: none, 32 or more: all).
 __device__ __forceinline__ uint32_t bits_below(int n) {
   return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
@@ -128,10 +134,12 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
 
 // One softmax step of a row: 128 scores at taddr -> P (bf16 pairs) over them.
 // [a, e): the row's window relative to the tile, k: its sinks relative to it;
-// `whole`: every key of the tile is visible to every row of the warp.
+// `whole`: every key of the tile is visible to every row of the warp; gone:
+// bits of the keys that do not exist, or null.
 template <int D>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, bool first, bool whole, int a, int e, int k,
-                                             float scale_log2, float& m_run, float& l_run) {
+                                             float scale_log2, float& m_run, float& l_run,
+                                             const uint32_t* gone = nullptr) {
   float s[kWTile];
   {
     uint32_t v[8][16];
@@ -148,7 +156,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, bool firs
     // not to branches.
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const uint32_t seen = bits_below(e - 32 * c) & (~bits_below(a - 32 * c) | bits_below(k - 32 * c));
+      uint32_t seen = bits_below(e - 32 * c) & (~bits_below(a - 32 * c) | bits_below(k - 32 * c));
+      if (gone) seen &= ~gone[c];
 #pragma unroll
       for (int j = 0; j < 32; ++j) s[32 * c + j] = (seen >> j) & 1u ? s[32 * c + j] : -INFINITY;
     }

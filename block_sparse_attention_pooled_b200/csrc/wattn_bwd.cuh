@@ -98,25 +98,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&pk)[3
   tmem_st_wait();
 }
 
-// 16 (D / 8) byte pieces of a row of D floats times f, as bf16.
-template <int D>
-__device__ __forceinline__ void store_row(__nv_bfloat16* out, uint32_t taddr, float f, bool zero, bool store) {
-#pragma unroll 1
-  for (int c = 0; c < D; c += 32) {
-    float o[32];
-    tmem_ld32(taddr + c, o);
-    tmem_ld_wait();
-    uint32_t w[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = zero ? 0u : pack_bf16x2(o[2 * j] * f, o[2 * j + 1] * f);
-    if (store) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4*>(out + c + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-    }
-  }
-}
-
 template <int D>
 __device__ __forceinline__ void store_zero(__nv_bfloat16* out) {
 #pragma unroll

@@ -183,7 +183,7 @@ sparge_status check_cache(const sparge_cache* c, const sparge_cache_batch* b, Ca
   if (c->d != 64 && c->d != 128) return SPARGE_ERR_UNSUPPORTED;
   if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return SPARGE_ERR_UNSUPPORTED;
   if (!all_aligned16({c->k, c->v})) return SPARGE_ERR_INVALID_ARG;
-  if (c->type == SPARGE_CACHE_E4M3 && (c->k_exp == nullptr || c->v_exp == nullptr)) return SPARGE_ERR_INVALID_ARG;
+  if (c->type == SPARGE_CACHE_E4M3 && !all_aligned16({c->k_exp, c->v_exp})) return SPARGE_ERR_INVALID_ARG;
   if (!b->page_table || !b->first || !b->cu) return SPARGE_ERR_INVALID_ARG;
   if ((int64_t)c->pages * c->Hkv > INT32_MAX || c->Hkv > 65535) return SPARGE_ERR_UNSUPPORTED;
   if ((int64_t)b->tokens * c->Hkv * 2 > INT32_MAX) return SPARGE_ERR_UNSUPPORTED;
@@ -201,6 +201,88 @@ sparge_status check_cache(const sparge_cache* c, const sparge_cache_batch* b, Ca
   v->max_pages = b->max_pages;
   v->tokens = b->tokens;
   return SPARGE_OK;
+}
+
+// Which kernel, and its workspace: per CTA a first and a last partial of `rows` rows.
+struct AttnPlan {
+  int rows;  // 8, 16: cache_decode_kernel; 256: cache_chunk_kernel
+  int tpt, ctas;
+  size_t bytes;
+};
+
+// Up to 16 rows a sequence the time is the cache's bytes and mma.sync keeps up
+// with them; more rows go to tcgen05, whose tiles have 128.
+AttnPlan attn_plan(const sparge_cache* c, const sparge_cache_batch* b, int32_t H, int32_t max_new) {
+  AttnPlan a;
+  const int64_t G = H / c->Hkv, rows = G * std::min(max_new, b->tokens);
+  a.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 2 * kWTile;
+  a.tpt = a.rows <= 16 ? (int)(a.rows / G) : (int)(kWTile / G) * 2;
+  a.ctas = sm_count();
+  a.bytes = align256((size_t)2 * a.ctas * a.rows * 8) + align256((size_t)2 * a.ctas * a.rows * c->d * 4);
+  return a;
+}
+
+// Pages [pages * Hkv][page][d] with boxes of a page's rows (64 at most): bf16
+// in 64-column boxes with the 128-byte swizzle, codes in whole rows with the
+// swizzle of their width.
+bool make_map_pages(CUtensorMap* m, const void* base, const sparge_cache* c) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const bool q = c->type == SPARGE_CACHE_E4M3;
+  const cuuint64_t width = q ? 1 : 2;
+  cuuint64_t dims[3] = {(cuuint64_t)c->d, (cuuint64_t)c->page, (cuuint64_t)c->pages * c->Hkv};
+  cuuint64_t strides[2] = {c->d * width, (cuuint64_t)c->page * c->d * width};
+  cuuint32_t box[3] = {q ? (cuuint32_t)c->d : 64, (cuuint32_t)std::min(c->page, 64), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, q ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            q && c->d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Q as [Hkv][tokens][G][d] with (64 channels x G heads x tq tokens) boxes.
+bool make_map_q(CUtensorMap* m, const CacheAttnParams& p, int d, int tq) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)p.G, (cuuint64_t)p.c.tokens, (cuuint64_t)p.c.Hkv};
+  cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)p.q_stride * 2, (cuuint64_t)p.G * d * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)p.G, (cuuint32_t)tq, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<__nv_bfloat16*>(p.Q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool E4M3, int R8>
+cudaError_t launch_decode(const CUtensorMap& mk, const CUtensorMap& mv, const CacheAttnParams& p, cudaStream_t st) {
+  using L = DecSmem<D, E4M3, R8>;
+  cudaError_t e = ensure_smem(cache_decode_kernel<D, E4M3, R8>, L::kBytes, (D == 64 ? 0 : 4) + (E4M3 ? 2 : 0) + R8 - 1 + 32);
+  if (e != cudaSuccess) return e;
+  cache_decode_kernel<D, E4M3, R8><<<p.ctas, L::kThreads, L::kBytes, st>>>(mk, mv, p);
+  return cudaGetLastError();
+}
+
+template <int D, bool E4M3>
+sparge_status launch_cache_attn(const sparge_cache* c, const CacheAttnParams& p, const AttnPlan& plan, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  if (!make_map_pages(&mk, c->k, c) || !make_map_pages(&mv, c->v, c)) return SPARGE_ERR_CUDA;
+  const unsigned join = (unsigned)ceil_div((int64_t)p.c.tokens * p.c.Hkv, 4);
+  cudaError_t e;
+  if (plan.rows <= 16) {
+    e = plan.rows == 8 ? launch_decode<D, E4M3, 1>(mk, mv, p, st) : launch_decode<D, E4M3, 2>(mk, mv, p, st);
+    if (e != cudaSuccess) return cuda_status(e);
+    cache_combine_kernel<D, kDecKeys><<<join, 128, 0, st>>>(p, plan.rows);
+    return cuda_status(cudaGetLastError());
+  }
+  CUtensorMap mq;
+  if (!make_map_q(&mq, p, D, plan.tpt / 2)) return SPARGE_ERR_CUDA;
+  e = ensure_smem(cache_chunk_kernel<D, E4M3>, WSmem<D>::kBytes, 40 + (D == 64 ? 0 : 2) + (E4M3 ? 1 : 0));
+  if (e != cudaSuccess) return cuda_status(e);
+  cache_chunk_kernel<D, E4M3><<<p.ctas, chunk_threads<E4M3>(), WSmem<D>::kBytes, st>>>(mq, mk, mv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_status(e);
+  cache_combine_kernel<D, kWTile><<<join, 128, 0, st>>>(p, plan.rows);
+  return cuda_status(cudaGetLastError());
 }
 
 }  // namespace
@@ -287,8 +369,10 @@ sparge_status sparge_cache_read(const sparge_cache* cache, const sparge_cache_ba
 
 size_t sparge_cache_attn_workspace_bytes(const sparge_cache* cache, const sparge_cache_batch* batch, int32_t H,
                                          int32_t max_new, int32_t max_len, const sparge_window* window) {
-  (void)cache, (void)batch, (void)H, (void)max_new, (void)max_len, (void)window;
-  return 0;
+  CacheView v;
+  if (check_cache(cache, batch, &v) != SPARGE_OK) return 0;
+  if (!window_ok(window) || H <= 0 || H % cache->Hkv || max_new < 1 || max_len < 1 || batch->tokens == 0) return 0;
+  return attn_plan(cache, batch, H, max_new).bytes;
 }
 
 sparge_status sparge_cache_attn(const sparge_cache* cache, const sparge_cache_batch* batch, const void* Q,
@@ -299,30 +383,28 @@ sparge_status sparge_cache_attn(const sparge_cache* cache, const sparge_cache_ba
   sparge_status st = check_cache(cache, batch, &p.c);
   if (st != SPARGE_OK) return st;
   if (!window_ok(window) || H <= 0 || H % cache->Hkv || max_new < 1 || max_len < 1) return SPARGE_ERR_INVALID_ARG;
-  if ((int64_t)batch->tokens * H > INT32_MAX) return SPARGE_ERR_UNSUPPORTED;
+  if ((int64_t)batch->tokens * H > INT32_MAX || H / cache->Hkv > kWTile) return SPARGE_ERR_UNSUPPORTED;
   if (batch->tokens == 0) return SPARGE_OK;
   if (!all_aligned16({Q, O}) || q_stride < (int64_t)H * cache->d || q_stride % 8) return SPARGE_ERR_INVALID_ARG;
-  st = check_ws(workspace, workspace_bytes,
-                sparge_cache_attn_workspace_bytes(cache, batch, H, max_new, max_len, window));
+  const AttnPlan plan = attn_plan(cache, batch, H, max_new);
+  st = check_ws(workspace, workspace_bytes, plan.bytes);
   if (st != SPARGE_OK) return st;
   p.w = device_window(window);
   p.Q = static_cast<const __nv_bfloat16*>(Q);
   p.q_stride = q_stride;
   p.O = static_cast<__nv_bfloat16*>(O);
   p.lse = lse;
+  p.part_ml = static_cast<float2*>(workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256((size_t)2 * plan.ctas * plan.rows * 8));
   p.H = H;
-  p.scale = (float)(1.0 / std::sqrt((double)cache->d));
-  const unsigned grid = (unsigned)ceil_div((int64_t)batch->tokens * H, 4);
+  p.G = H / cache->Hkv;
+  p.tpt = plan.tpt;
+  p.ctas = plan.ctas;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)cache->d));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool q = cache->type == SPARGE_CACHE_E4M3;
-  if (cache->d == 64) {
-    if (q) cache_attn_simple<64, true><<<grid, 128, 0, s>>>(p);
-    else cache_attn_simple<64, false><<<grid, 128, 0, s>>>(p);
-  } else {
-    if (q) cache_attn_simple<128, true><<<grid, 128, 0, s>>>(p);
-    else cache_attn_simple<128, false><<<grid, 128, 0, s>>>(p);
-  }
-  return cuda_status(cudaGetLastError());
+  if (cache->d == 64) return q ? launch_cache_attn<64, true>(cache, p, plan, s) : launch_cache_attn<64, false>(cache, p, plan, s);
+  return q ? launch_cache_attn<128, true>(cache, p, plan, s) : launch_cache_attn<128, false>(cache, p, plan, s);
 }
 
 }  // extern "C"

@@ -393,7 +393,7 @@ sparge_status sparge_cache_read(const sparge_cache* cache, const sparge_cache_ba
  * position first[b] + t, and L = first[b] + the number of its new tokens.
  *   Q           bf16 [tokens, H, d], token t's row at Q + t * q_stride (elements,
  *               a multiple of 8), heads contiguous.
- *   H           query heads, a multiple of cache->Hkv.
+ *   H           query heads, a multiple of cache->Hkv, at most 128 times it.
  *   max_new, max_len  bounds of a sequence's new tokens and of L, >= 1. They
  *               choose how the work is split, not what is computed.
  *   O           bf16 [tokens, H, d], contiguous;  lse: optional float [tokens, H].
