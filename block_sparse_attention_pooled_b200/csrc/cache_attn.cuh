@@ -31,7 +31,7 @@ constexpr int kDecKeys = 64;  // keys per tile
 
 template <int D, bool E4M3, int R8>
 struct DecSmem {
-  static constexpr int NW = E4M3 ? 8 : 4;                // consumer warps
+  static constexpr int NW = E4M3 ? (R8 == 1 ? 6 : 5) : D == 128 ? 3 : 4;  // consumer warps
   static constexpr int kRows = 8 * R8;
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kTile = kDecKeys * kRowBytes;     // K or V
@@ -39,7 +39,12 @@ struct DecSmem {
   static constexpr int kOStride = D + 4;                 // floats; + 4: the lanes' rows fall into different banks
   static constexpr int kMerge = NW * kRows * (kOStride * 4 + 8);
   static constexpr int kBudget = 225 * 1024 - kMerge - 2048;
-  static constexpr int NS = kBudget / (kStage + 160) > 16 ? 16 : kBudget / (kStage + 160);
+  // A multiple of the warps, so that a slot is always the same warp's: a warp
+  // that met a slot first in a later round could take the round before, still
+  // on its way, for its own (the barrier tells odd rounds from even ones only).
+  static constexpr int kFit = kBudget / (kStage + 160);
+  static constexpr int NS = (kFit > 16 ? 16 : kFit) / NW * NW;
+  static_assert(NS >= 2 * NW || NS >= 4);
   static constexpr int kOffExp = NS * kStage;            // per stage: K's and V's powers, 64 bytes each
   static constexpr int kOffMask = kOffExp + NS * 128;    // per stage: which 16-key groups exist
   static constexpr int kOffBar = kOffMask + NS * 4 + (NS & 1) * 4;
@@ -451,7 +456,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
     const bool all = at0 == 0 && stop == it.T;
     const int64_t slot0 = (int64_t)(2 * blockIdx.x + (start < unit0 ? 1 : 0)) * L::kRows;
     constexpr int TPR = D / 4;  // threads per row, four channels each
-    for (int r = threadIdx.x / TPR; r < tokens * p.G; r += NW * 32 / TPR) {
+    for (int r = threadIdx.x / TPR; r < tokens * p.G; r += NW * 32 / TPR) {  // NW * 32 is a multiple of TPR
       const int ch = (threadIdx.x % TPR) * 4;
       float m = -INFINITY, l = 0.0f;
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);

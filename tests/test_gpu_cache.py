@@ -321,3 +321,25 @@ def test_a_clip_generated_frame_by_frame(sparge, d):
                 o, _, to, _, _ = rows_fwd(Q[b, h, now], K[b, h // 2], V[b, h // 2], seen[now])
                 close(O[b, h], o, to, f"frame {f}")
                 close(whole[b, h, now], o, to, f"frame {f} of the whole clip")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H", [8, 16, 32])
+def test_a_large_batch_again_and_again(sparge, kind, H):
+    """More sequences than lanes, runs that cross many items, calls back to back: every call gives the same bits."""
+    Hkv, d, past = 4, 128, [3000 + 131 * b for b in range(40)]
+    c = Paged(kind, Hkv, d, 64, [p + 1 for p in past])
+    ks, vs = c.fill(sparge, [p + 1 for p in past])
+    Q = c.normal(40, H, d)
+    cu, first = torch.arange(41, dtype=torch.int32, device="cuda"), ints(*past)
+    runs = [sparge.sparge_cache_attn(Q, c.k, c.v, c.table, first, cu, 1, max(past) + 1, **c.exp) for _ in range(20)]
+    torch.cuda.synchronize()
+    assert sparge.device_status() == 0
+    for o in runs[1:]:
+        assert torch.equal(o, runs[0])
+    for b in (0, 17, 31, 32, 39):
+        at = torch.arange(past[b] + 1, device="cuda")
+        seen = visible(at[-1:], at, past[b] + 1, *CAUSAL)
+        for h in range(0, H, 3):
+            o, _, to, _, _ = rows_fwd(Q[b:b + 1, h], ks[b][h // (H // Hkv)], vs[b][h // (H // Hkv)], seen)
+            close(runs[0][b:b + 1, h], o, to, f"sequence {b}, head {h}")
