@@ -31,7 +31,11 @@ constexpr int kDecKeys = 64;  // keys per tile
 
 template <int D, bool E4M3, int R8>
 struct DecSmem {
-  static constexpr int NW = E4M3 ? (R8 == 1 ? 6 : 5) : D == 128 ? 3 : 4;  // consumer warps
+  // Consumer warps; SPLIT of them share a tile, each with its part of the keys.
+  // bf16: the tensor instructions and ldmatrix of three warps keep up with
+  // memory. e4m3: half the bytes and ten instructions per four codes need more.
+  static constexpr int SPLIT = E4M3 ? 2 : 1;
+  static constexpr int NW = E4M3 ? (R8 == 1 ? 10 : 8) : D == 128 ? 3 : 4;
   static constexpr int kRows = 8 * R8;
   static constexpr int kRowBytes = D * (E4M3 ? 1 : 2);
   static constexpr int kTile = kDecKeys * kRowBytes;     // K or V
@@ -39,12 +43,12 @@ struct DecSmem {
   static constexpr int kOStride = D + 4;                 // floats; + 4: the lanes' rows fall into different banks
   static constexpr int kMerge = NW * kRows * (kOStride * 4 + 8);
   static constexpr int kBudget = 225 * 1024 - kMerge - 2048;
-  // A multiple of the warps, so that a slot is always the same warp's: a warp
+  // A multiple of the warps' turns, so that a slot is always the same warp's: a warp
   // that met a slot first in a later round could take the round before, still
   // on its way, for its own (the barrier tells odd rounds from even ones only).
   static constexpr int kFit = kBudget / (kStage + 160);
-  static constexpr int NS = (kFit > 16 ? 16 : kFit) / NW * NW;
-  static_assert(NS >= 2 * NW || NS >= 4);
+  static constexpr int NS = (kFit > 16 ? 16 : kFit) / (NW / SPLIT) * (NW / SPLIT);
+  static_assert(NS >= 4);
   static constexpr int kOffExp = NS * kStage;            // per stage: K's and V's powers, 64 bytes each
   static constexpr int kOffMask = kOffExp + NS * 128;    // per stage: which 16-key groups exist
   static constexpr int kOffBar = kOffMask + NS * 4 + (NS & 1) * 4;
@@ -113,7 +117,8 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
     cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const CacheAttnParams p) {
   using L = DecSmem<D, E4M3, R8>;
-  constexpr int NS = L::NS, NW = L::NW, KT = kDecKeys;
+  constexpr int NS = L::NS, NW = L::NW, KT = kDecKeys, SPLIT = L::SPLIT;
+  constexpr int MT = KT / 16 / SPLIT;  // a warp's 16-key steps of a tile
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -129,7 +134,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full(i), 1);
-      mbar_init(empty(i), 1);
+      mbar_init(empty(i), SPLIT);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -151,10 +156,13 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
     while (ok && left > 0) {
       const int stop = (int)min((int64_t)it.T, at + left);
       left -= stop - at;
+      PageAhead<KT> pages;
+      pages.start(p, it, at, stop, lane);
       for (int t = at; t < stop; ++t, ++n) {
         const int slot = n % NS;
         const int pos = it.kt.key0(t) + (lane << box_shift);
-        const int64_t row = lane < boxes && pos < it.len() ? cache_row(p.c, it.b, pos) : -1;  // a page's row, head 0
+        int64_t row = pages.get(p, it, t, lane);  // a page's row, head 0
+        if (lane >= boxes) row = -1;
         ok = n < NS || role_wait(empty(slot), (n / NS - 1) & 1, kErrCaEmpty, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -200,6 +208,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
 
   // -------------------------------------------------------------- consumers
   const int g = lane >> 2, c = lane & 3;
+  const int turn = warp / SPLIT, k16 = warp % SPLIT * MT;  // its first 16-key step
   uint32_t n = 0;
   bool ok = true;
   while (ok && left > 0) {
@@ -249,7 +258,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
     const int all_lo = p.w.lo(it.first + t0 + tokens - 1), all_hi = p.w.hi(it.first + t0, len);
 
     for (int t = at; t < stop; ++t, ++n) {
-      if (n % NW != warp) continue;
+      if (n % (NW / SPLIT) != turn) continue;
       const int slot = n % NS, key0 = it.kt.key0(t);
       const bool sink = t < it.kt.ns;
       ok = __all_sync(0xffffffffu, role_wait(full(slot), (n / NS) & 1, kErrCaFull, abort_flag));
@@ -272,9 +281,9 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
         __syncwarp();
       }
       // S^T
-      float s[KT / 16][R8][4];
+      float s[MT][R8][4];
 #pragma unroll
-      for (int mt = 0; mt < KT / 16; ++mt) {
+      for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int x = 0; x < R8; ++x)
 #pragma unroll
@@ -285,7 +294,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
             uint32_t w[2][4];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const int r = 16 * mt + g + 8 * y, ch = 4 * j + c;
+              const int r = 16 * (k16 + mt) + g + 8 * y, ch = 4 * j + c;
               const uint4 v = lds128(sk + r * D + (D == 128 ? (ch ^ (r & 7)) : (ch ^ ((r >> 1) & 3))) * 16);
               w[y][0] = v.x, w[y][1] = v.y, w[y][2] = v.z, w[y][3] = v.w;
             }
@@ -301,7 +310,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
         } else {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const int r = 16 * mt + (lane & 15), ch = 2 * k + (lane >> 4);
+            const int r = 16 * (k16 + mt) + (lane & 15), ch = 2 * k + (lane >> 4);
             uint32_t a[4];
             ldsm4(sk + (ch / 8) * (KT * 128) + r * 128 + (((ch % 8) ^ (r & 7)) * 16), a);
 #pragma unroll
@@ -310,14 +319,14 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
         }
       }
       // To log2 units; keys that a row does not see to -inf.
-      float pv[KT / 16][2];  // e4m3: V's powers of the lane's keys
+      float pv[MT][2];  // e4m3: V's powers of the lane's keys
 #pragma unroll
-      for (int mt = 0; mt < KT / 16; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           float f = p.scale_log2;
           if (E4M3) {
-            const int r = 16 * mt + g + 8 * z;
+            const int r = 16 * (k16 + mt) + g + 8 * z;
             f *= exp_scale((uint8_t)lds_u8(ex + r));
             pv[mt][z] = exp_scale((uint8_t)lds_u8(ex + 64 + r));
           }
@@ -329,11 +338,11 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
       if (!whole) {
         const int most = sink ? it.kt.cut : len;
 #pragma unroll
-        for (int mt = 0; mt < KT / 16; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            const int j = key0 + 16 * mt + g + 8 * z;
-            const bool here = (mask >> mt & 1u) && j < most;
+            const int j = key0 + 16 * (k16 + mt) + g + 8 * z;
+            const bool here = (mask >> (k16 + mt) & 1u) && j < most;
 #pragma unroll
             for (int x = 0; x < R8; ++x)
 #pragma unroll
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
           }
       }
       // Running maximum and sum; P^T as operand B, two 16-bit keys a register.
-      uint32_t b[KT / 16][R8][2];
+      uint32_t b[MT][R8][2];
 #pragma unroll
       for (int x = 0; x < R8; ++x) {
         float top[2];
@@ -352,7 +361,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
         for (int y = 0; y < 2; ++y) {
           float m = fmaxf(s[0][x][y], s[0][x][2 + y]);
 #pragma unroll
-          for (int mt = 1; mt < KT / 16; ++mt) m = fmax3(m, s[mt][x][y], s[mt][x][2 + y]);
+          for (int mt = 1; mt < MT; ++mt) m = fmax3(m, s[mt][x][y], s[mt][x][2 + y]);
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
           top[y] = fmaxf(m, m_run[x][y]);
@@ -374,7 +383,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
         for (int y = 0; y < 2; ++y) {
           const float ref = m_run[x][y] == -INFINITY ? 0.0f : m_run[x][y];
 #pragma unroll
-          for (int mt = 0; mt < KT / 16; ++mt)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
               float e = ex2_approx(s[mt][x][2 * z + y] - ref);
@@ -384,20 +393,20 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
             }
         }
 #pragma unroll
-        for (int mt = 0; mt < KT / 16; ++mt) {
+        for (int mt = 0; mt < MT; ++mt) {
           b[mt][x][0] = movmatrix_t(pack_bf16x2(s[mt][x][0], s[mt][x][1]));
           b[mt][x][1] = movmatrix_t(pack_bf16x2(s[mt][x][2], s[mt][x][3]));
         }
       }
       // O^T
 #pragma unroll
-      for (int mt = 0; mt < KT / 16; ++mt) {
+      for (int mt = 0; mt < MT; ++mt) {
         if (E4M3) {
           constexpr int NB = D / 8;  // codes per lane and key row
           uint32_t w[4][NB / 4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const int r = 16 * mt + 2 * c + (y & 1) + 8 * (y >> 1);
+            const int r = 16 * (k16 + mt) + 2 * c + (y & 1) + 8 * (y >> 1);
             if (D == 128) {
               const uint4 v = lds128(sv + r * D + ((g ^ (r & 7)) * 16));
               w[y][0] = v.x, w[y][1] = v.y, w[y][NB / 4 - 2] = v.z, w[y][NB / 4 - 1] = v.w;
@@ -424,7 +433,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
         } else {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const int r = 16 * mt + (lane & 7) + 8 * (lane >> 4), ch = 2 * k + ((lane >> 3) & 1);
+            const int r = 16 * (k16 + mt) + (lane & 7) + 8 * (lane >> 4), ch = 2 * k + ((lane >> 3) & 1);
             uint32_t a[4];
             ldsm4_t(sv + (ch / 8) * (KT * 128) + r * 128 + (((ch % 8) ^ (r & 7)) * 16), a);
 #pragma unroll

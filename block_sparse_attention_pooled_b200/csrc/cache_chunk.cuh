@@ -103,10 +103,13 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
       ++nq;
       if (!E4M3) {
         const int box_shift = min(p.c.page_shift, 6), boxes = KT >> box_shift, len = it.len();
+        PageAhead<KT> pages;
+        pages.start(p, it, at, stop, lane);
         for (int t = 2 * at; ok && t < 2 * stop; ++t, ++n) {  // K(0), V(0), K(1), V(1), ...
           const int slot = n % NS, key0 = it.kt.key0(t >> 1);
           const int pos = key0 + (lane << box_shift);
-          const int64_t row = lane < boxes && pos < len ? cache_row(p.c, it.b, pos) : -1;
+          int64_t row = pages.get(p, it, t >> 1, lane);
+          if (lane >= boxes) row = -1;
           ok = n < NS || role_wait(bar(L::kBarKvEmpty + slot), (n / NS - 1) & 1, kErrCcKvEmpty, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -238,23 +241,26 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
       const int lo = p.w.lo(i), hi = p.w.hi(i, len);
       const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
       float m_run = -INFINITY, l_run = 0.0f;
+      // Lane l < 8: whether the tile's l-th 16 keys lie in a page that does not
+      // exist; looked up a tile ahead.
+      auto absent = [&](int t) {
+        const int g16 = it.kt.key0(t) + lane * 16;
+        return lane < 8 && t < stop && g16 < len && cache_row(p.c, it.b, g16) < 0;
+      };
+      bool next_absent = absent(at);
       for (int t = at; t < stop; ++t, ++np) {
         const int key0 = it.kt.key0(t);
-        // Keys of pages that do not exist.
-        uint32_t gone[4] = {0, 0, 0, 0};
-        if (t < it.kt.total || it.kt.total == 0) {
-          const int g16 = key0 + lane * 16;
-          const bool absent = lane < 8 && g16 < len && cache_row(p.c, it.b, g16) < 0;
-          const unsigned m = __ballot_sync(0xffffffffu, absent);
+        const unsigned m = __ballot_sync(0xffffffffu, next_absent);
+        next_absent = absent(t + 1);
+        uint32_t gone[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            gone[c] = ((m >> (2 * c)) & 1u ? 0xFFFFu : 0u) | ((m >> (2 * c + 1)) & 1u ? 0xFFFF0000u : 0u);
-        }
+        for (int c = 0; c < 4; ++c)
+          gone[c] = ((m >> (2 * c)) & 1u ? 0xFFFFu : 0u) | ((m >> (2 * c + 1)) & 1u ? 0xFFFF0000u : 0u);
         ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarS + x), np & 1, kErrCcS, abort_flag));
         if (!ok) break;
         tc_fence_after();
         const bool sink = t < it.kt.ns;
-        const bool whole = (gone[0] | gone[1] | gone[2] | gone[3]) == 0 &&
+        const bool whole = m == 0 &&
                            (sink ? key0 + KT <= min(it.kt.cut, all_hi) : key0 >= all_lo && key0 + KT <= all_hi);
         const int e = (sink ? min(hi, it.kt.cut) : hi) - key0;
         softmax_tile<D>(ts, to, t == at, whole, sink ? 0 : lo - key0, e, p.w.sinks - key0, p.scale_log2, m_run, l_run,

@@ -181,6 +181,41 @@ __device__ __forceinline__ CacheItem<KT> find_unit(const CacheAttnParams& p, int
   return found;
 }
 
+// The page rows (cache_row) of an item's key tiles, a batch of tiles at a time:
+// lane l holds box l % boxes of tile `base` + l / boxes, and the next batch is
+// on its way, so no tile waits for the page table (its latency, once a tile,
+// is as long as a tile's own bytes take).
+template <int KT>
+struct PageAhead {
+  int boxes_shift, box_shift, base, stop;
+  int64_t cur, nxt;
+  __device__ __forceinline__ int64_t fetch(const CacheAttnParams& p, const CacheItem<KT>& it, int from, int lane) const {
+    const int t = from + (lane >> boxes_shift);
+    const int pos = it.kt.key0(t) + ((lane & ((1 << boxes_shift) - 1)) << box_shift);
+    return t < stop && pos < it.len() ? cache_row(p.c, it.b, pos) : -1;
+  }
+  __device__ __forceinline__ int tiles() const { return 32 >> boxes_shift; }
+  // Tiles at .. end - 1 of the item.
+  __device__ __forceinline__ void start(const CacheAttnParams& p, const CacheItem<KT>& it, int at, int end, int lane) {
+    box_shift = min(p.c.page_shift, 6);
+    boxes_shift = 31 - __clz(KT) - box_shift;
+    base = at;
+    stop = end;
+    cur = fetch(p, it, base, lane);
+    nxt = fetch(p, it, base + tiles(), lane);
+  }
+  // The row of box `lane` of tile t (lanes past the boxes: of some other box);
+  // t does not decrease.
+  __device__ __forceinline__ int64_t get(const CacheAttnParams& p, const CacheItem<KT>& it, int t, int lane) {
+    if (t >= base + tiles()) {
+      base += tiles();
+      cur = nxt;
+      nxt = fetch(p, it, base + tiles(), lane);
+    }
+    return __shfl_sync(0xffffffffu, cur, (((t - base) << boxes_shift) + lane) & 31);
+  }
+};
+
 // CTAs that get a run: two units at least, so that a short cache does not end
 // up in more partials than tiles.
 __device__ __forceinline__ int ctas_used(int64_t W, int ctas) { return (int)max((int64_t)1, min((int64_t)ctas, W / 2)); }
