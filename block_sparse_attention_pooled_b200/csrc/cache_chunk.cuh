@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
-      const bool rows = (i >= L::kBarP && i < L::kBarP + 2) || (i >= L::kBarOFree && i < L::kBarOFree + 2);
+      const bool rows = (i >= L::kBarP && i < L::kBarP + 4) || (i >= L::kBarOFree && i < L::kBarOFree + 2);
       const bool conv = E4M3 && i >= L::kBarKvFull && i < L::kBarKvFull + NS;
       mbar_init(bar(i), rows || conv ? 128 : 1);
     }
@@ -196,8 +196,18 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
           if (leader) {
             const uint64_t v = dVm + (uint64_t)((vs * L::kTileBytes) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kWTile / 16; ++kk)
+            for (int kk = 0; kk < kWTile / 32; ++kk)
               mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, v + kk * 128, idO, (t > 0 || kk > 0) ? 1u : 0u);
+          }
+          __syncwarp();
+          ok = wait(L::kBarP2 + x, np & 1, kErrCcP);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t v = dVm + (uint64_t)((vs * L::kTileBytes) >> 4);
+#pragma unroll
+            for (int kk = kWTile / 32; kk < kWTile / 16; ++kk)
+              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, v + kk * 128, idO, 1u);
             if (x == 1) mma_commit(bar(L::kBarKvEmpty + vs));
             if (!more) mma_commit(bar(L::kBarO + x));
           }
@@ -264,9 +274,12 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
                            (sink ? key0 + KT <= min(it.kt.cut, all_hi) : key0 >= all_lo && key0 + KT <= all_hi);
         const int e = (sink ? min(hi, it.kt.cut) : hi) - key0;
         softmax_tile<D>(ts, to, t == at, whole, sink ? 0 : lo - key0, e, p.w.sinks - key0, p.scale_log2, m_run, l_run,
-                        gone);
+                        gone, [&] {
+                          tc_fence_before();
+                          mbar_arrive(bar(L::kBarP + x));
+                        });
         tc_fence_before();
-        mbar_arrive(bar(L::kBarP + x));
+        mbar_arrive(bar(L::kBarP2 + x));
       }
       if (!ok) break;
       ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarO + x), nq & 1, kErrCcO, abort_flag));

@@ -60,8 +60,9 @@ struct WSmem {
   static constexpr int kOffKv = 2 * kTileBytes;
   static constexpr int kOffBar = kOffKv + NS * kTileBytes;
   static constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarKvFull = 2, kBarKvEmpty = 2 + NS, kBarS = 2 + 2 * NS,
-                       kBarP = 4 + 2 * NS, kBarO = 6 + 2 * NS, kBarOFree = 8 + 2 * NS, kBarDrain = 10 + 2 * NS;
-  static constexpr int kNumBars = 11 + 2 * NS;
+                       kBarP = 4 + 2 * NS, kBarP2 = 6 + 2 * NS, kBarO = 8 + 2 * NS, kBarOFree = 10 + 2 * NS,
+                       kBarDrain = 12 + 2 * NS;
+  static constexpr int kNumBars = 13 + 2 * NS;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffTmem + 16 + 1024;
 };
@@ -132,14 +133,72 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
   return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
+// 2^x for two lanes on the FMA and integer pipes, as exp2_poly2 with one more
+// term (the same fit in degree 4): relative error at most 2.7e-6, so that the
+// row sums, and with them the log-sum-exp, keep 32-bit quality.
+__device__ __forceinline__ uint64_t exp2_poly4(uint64_t x) {
+  const uint64_t magic = f2(12582912.0f, 12582912.0f);
+  const uint64_t t = add2(x, magic);
+  const uint64_t f = sub2(x, sub2(t, magic));
+  uint64_t p = fma2(f2(0.009570102207f, 0.009570102207f), f, f2(0.05591785908f, 0.05591785908f));
+  p = fma2(p, f, f2(0.2402474433f, 0.2402474433f));
+  p = fma2(p, f, f2(0.6931217909f, 0.6931217909f));
+  p = fma2(p, f, f2(0.9999992847f, 0.9999992847f));
+  const float2 tv = f2_split(t), pv = f2_split(p);
+  constexpr int kMinBits = 0x4B400000 - 125;
+  const uint32_t lo = __float_as_uint(pv.x) + ((uint32_t)max(__float_as_int(tv.x), kMinBits) << 23);
+  const uint32_t hi = __float_as_uint(pv.y) + ((uint32_t)max(__float_as_int(tv.y), kMinBits) << 23);
+  return f2(__uint_as_float(lo), __uint_as_float(hi));
+}
+
+// Of every 16 pairs of exponentials, so many take the polynomial.
+#ifndef SPARGE_WPOLY
+#define SPARGE_WPOLY 4
+#endif
+constexpr int kWPoly = SPARGE_WPOLY;
+
+// 2^(s scale - ref) -> P (bf16 pairs) over the scores' columns; the row's sum.
+// half() runs when the first 64 keys' P is in TMEM.
+template <int POLY, typename Half>
+__device__ __forceinline__ float exp_store(const float (&s)[kWTile], uint32_t ts, float scale_log2, float ref, Half half) {
+  const uint64_t scale2 = f2(scale_log2, scale_log2), negm2 = f2(-ref, -ref);
+  uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint64_t x = fma2(f2(s[32 * c + 2 * j], s[32 * c + 2 * j + 1]), scale2, negm2);
+      uint64_t ex;
+      if (POLY > 0 && j % (POLY > 0 ? 16 / POLY : 1) == 1) {  // spread among the others
+        ex = exp2_poly4(x);
+      } else {
+        const float2 xv = f2_split(x);
+        ex = f2(ex2_approx(xv.x), ex2_approx(xv.y));
+      }
+      acc[j & 3] = add2(acc[j & 3], ex);
+      const float2 ev = f2_split(ex);
+      pk[j] = pack_bf16x2(ev.x, ev.y);
+    }
+    tmem_st16(ts + 16 * c, pk);
+    if (c == 1) {
+      tmem_st_wait();
+      half();
+    }
+  }
+  const float2 t = f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])));
+  tmem_st_wait();
+  return t.x + t.y;
+}
+
 // One softmax step of a row: 128 scores at taddr -> P (bf16 pairs) over them.
 // [a, e): the row's window relative to the tile, k: its sinks relative to it;
 // `whole`: every key of the tile is visible to every row of the warp; gone:
 // bits of the keys that do not exist, or null.
-template <int D>
+template <int D, typename Half>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, bool first, bool whole, int a, int e, int k,
-                                             float scale_log2, float& m_run, float& l_run,
-                                             const uint32_t* gone = nullptr) {
+                                             float scale_log2, float& m_run, float& l_run, const uint32_t* gone,
+                                             Half half) {
   float s[kWTile];
   {
     uint32_t v[8][16];
@@ -183,24 +242,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, bool firs
     m_run = m_new;
   }
   const float ref = m_run == -INFINITY ? 0.0f : m_run;
-  const uint64_t scale2 = f2(scale_log2, scale_log2), negm2 = f2(-ref, -ref);
-  uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t pk[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float2 x = f2_split(fma2(f2(s[32 * c + 2 * j], s[32 * c + 2 * j + 1]), scale2, negm2));
-      const uint64_t ex = f2(ex2_approx(x.x), ex2_approx(x.y));
-      acc[j & 3] = add2(acc[j & 3], ex);
-      const float2 ev = f2_split(ex);
-      pk[j] = pack_bf16x2(ev.x, ev.y);
-    }
-    tmem_st16(ts + 16 * c, pk);
-  }
-  const float2 t = f2_split(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])));
-  l_run += t.x + t.y;
-  tmem_st_wait();
+  l_run += whole ? exp_store<kWPoly>(s, ts, scale_log2, ref, half) : exp_store<0>(s, ts, scale_log2, ref, half);
 }
 
 template <int D>
@@ -221,7 +263,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
-      const bool rows = (i >= L::kBarP && i < L::kBarP + 2) || (i >= L::kBarOFree && i < L::kBarOFree + 2);
+      const bool rows = (i >= L::kBarP && i < L::kBarP + 4) || (i >= L::kBarOFree && i < L::kBarOFree + 2);
       mbar_init(bar(i), rows ? 128 : 1);
     }
     *abort_flag = 0;
@@ -353,8 +395,18 @@ __global__ void __launch_bounds__(kWThreads, 1)
           if (leader) {
             const uint64_t v = dVm + (uint64_t)((vs * L::kTileBytes) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kWTile / 16; ++kk)  // 16 keys = 2048 bytes of V = 8 columns of P
+            for (int kk = 0; kk < kWTile / 32; ++kk)  // 16 keys = 2048 bytes of V = 8 columns of P
               mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, v + kk * 128, idO, (t > 0 || kk > 0) ? 1u : 0u);
+          }
+          __syncwarp();
+          ok = wait(L::kBarP2 + x, np & 1, kErrWinP);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t v = dVm + (uint64_t)((vs * L::kTileBytes) >> 4);
+#pragma unroll
+            for (int kk = kWTile / 32; kk < kWTile / 16; ++kk)
+              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, v + kk * 128, idO, 1u);
             if (x == 1) mma_commit(bar(L::kBarKvEmpty + vs));
             if (!more) mma_commit(bar(L::kBarO + x));
           }
@@ -408,9 +460,13 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const bool sink = t < kt.ns;
         const bool whole = sink ? key0 + kWTile <= min(kt.cut, all_hi) : key0 >= all_lo && key0 + kWTile <= all_hi;
         const int e = (sink ? min(hi, kt.cut) : hi) - key0;
-        softmax_tile<D>(ts, to, t == 0, whole, sink ? 0 : lo - key0, e, p.w.sinks - key0, p.scale_log2, m_run, l_run);
+        softmax_tile<D>(ts, to, t == 0, whole, sink ? 0 : lo - key0, e, p.w.sinks - key0, p.scale_log2, m_run, l_run,
+                        nullptr, [&] {
+                          tc_fence_before();
+                          mbar_arrive(bar(L::kBarP + x));
+                        });
         tc_fence_before();
-        mbar_arrive(bar(L::kBarP + x));
+        mbar_arrive(bar(L::kBarP2 + x));
       }
       if (!ok) break;
       if (i >= len) l_run = 0.0f;
