@@ -1,8 +1,8 @@
 // Attention of few new tokens over the paged cache (one token of each of G
 // heads when decoding): bound by reading the cache once.
 //
-// Persistent CTAs with equal runs of 64-key tiles (cache_sched.cuh). A producer
-// warp fills a ring of K and V tiles by TMA through the page table (one box per
+// Persistent CTAs with equal runs of 64-key tiles (cache_sched.cuh). Two producer
+// warps fill a ring of K and V tiles by TMA through the page table (one box per
 // page and 64 columns; 128 bytes of swizzle); the other warps take whole tiles
 // in turn, each with a running maximum and sum and an accumulator of its own,
 // so that nothing but the ring orders them, and are joined in shared memory at
@@ -56,7 +56,7 @@ struct DecSmem {
   static constexpr int kOffO = (kOffMl + NW * kRows * 8 + 15) / 16 * 16;
   static constexpr int kOffAbort = kOffO + NW * kRows * kOStride * 4;
   static constexpr int kBytes = kOffAbort + 16 + 1024;
-  static constexpr int kThreads = (NW + 1) * 32;
+  static constexpr int kThreads = (NW + 2) * 32;
   static_assert(kBytes <= 227 * 1024);
 };
 
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full(i), 1);
+      mbar_init(full(i), 2);
       mbar_init(empty(i), SPLIT);
     }
     *abort_flag = 0;
@@ -148,8 +148,11 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
   CacheItem<KT> it = find_unit<KT>(p, start, lane, at);
   int64_t left = end - start;
 
-  if (warp == NW) {
-    // ------------------------------------------------------------ producer
+  if (warp >= NW) {
+    // ------------------------------------------------------------ producers: one warp for K, one for V
+    const bool is_v = warp > NW;
+    const CUtensorMap* tm = is_v ? &tmV : &tmK;
+    const uint8_t* exps = is_v ? p.c.v_exp : p.c.k_exp;
     const int box_shift = min(p.c.page_shift, 6), boxes = KT >> box_shift;  // keys per box: a page's, 64 at most
     uint32_t n = 0;
     bool ok = true;
@@ -168,31 +171,29 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
         if (!ok) break;
         const unsigned there = __ballot_sync(0xffffffffu, row >= 0);
         if (lane == 0) {
-          uint32_t m = 0;  // one bit per 16 keys
-          for (int x = 0; x < boxes; ++x)
-            if (there >> x & 1u) m |= ((1u << (1 << (box_shift - 4))) - 1u) << (x << (box_shift - 4));
-          masks[slot] = m;
+          if (!is_v) {
+            uint32_t m = 0;  // one bit per 16 keys
+            for (int x = 0; x < boxes; ++x)
+              if (there >> x & 1u) m |= ((1u << (1 << (box_shift - 4))) - 1u) << (x << (box_shift - 4));
+            masks[slot] = m;
+          }
           const uint32_t bytes = (uint32_t)__popc(there) << box_shift;
-          mbar_arrive_expect_tx(full(slot), bytes * (2 * L::kRowBytes + (E4M3 ? 2 : 0)));
+          mbar_arrive_expect_tx(full(slot), bytes * (L::kRowBytes + (E4M3 ? 1 : 0)));
         }
         __syncwarp();
         if (row >= 0) {
-          const uint32_t dst = sbase + slot * L::kStage + (lane << box_shift) * (E4M3 ? D : 128);
+          const uint32_t dst =
+              sbase + slot * L::kStage + (is_v ? L::kTile : 0) + (lane << box_shift) * (E4M3 ? D : 128);
           const int place = pos & ((1 << p.c.page_shift) - 1);
           const int64_t head = row + ((int64_t)it.hk << p.c.page_shift);
           const int z = (int)((head - place) >> p.c.page_shift);
           if (E4M3) {
-            tma_load_3d(dst, &tmK, full(slot), 0, place, z);
-            tma_load_3d(dst + L::kTile, &tmV, full(slot), 0, place, z);
-            const uint32_t ex = sbase + L::kOffExp + slot * 128 + (lane << box_shift);
-            bulk_load(ex, p.c.k_exp + head, 1u << box_shift, full(slot));
-            bulk_load(ex + 64, p.c.v_exp + head, 1u << box_shift, full(slot));
+            tma_load_3d(dst, tm, full(slot), 0, place, z);
+            bulk_load(sbase + L::kOffExp + slot * 128 + (is_v ? 64 : 0) + (lane << box_shift), exps + head,
+                      1u << box_shift, full(slot));
           } else {
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-              tma_load_3d(dst + c * (KT * 128), &tmK, full(slot), c * 64, place, z);
-              tma_load_3d(dst + c * (KT * 128) + L::kTile, &tmV, full(slot), c * 64, place, z);
-            }
+            for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * (KT * 128), tm, full(slot), c * 64, place, z);
           }
         }
         __syncwarp();

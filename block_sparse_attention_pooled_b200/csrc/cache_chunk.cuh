@@ -6,10 +6,11 @@
 // A row is a (token, head of the K/V head's group) pair, token by token, so a
 // tile holds 128 / G tokens and K and V are read once for the whole group. The
 // rows of Q come by a 4-D TMA box {64 channels, G heads, 128 / G tokens}.
-// K and V, bf16: by TMA, one box per page; a tile with places that do not exist
-// is copied by the producer's lanes, zeros there. e4m3: four more warps load
-// the codes (the next tile's while they convert this one's) and write them into
-// the ring as bf16, each times its row's power: exact.
+// K and V come by TMA, one box per page, from a warp each (a box costs its
+// issuing lane some hundred cycles). bf16: straight into the ring; a tile with
+// places that do not exist is copied by the warp's lanes, zeros there. e4m3:
+// the codes into a slot of their own, from where four more warps write them
+// into the ring as bf16, each times its row's power: exact.
 #pragma once
 #include <cuda.h>
 #include <cstdint>
@@ -25,14 +26,40 @@ enum : unsigned int {
   kErrCcQ = 0xC00, kErrCcQEmpty, kErrCcKvFull, kErrCcKvEmpty, kErrCcS, kErrCcP, kErrCcO, kErrCcOFree, kErrCcDrain
 };
 
+// Waits for a phase for a millisecond at most, and says nothing.
+__device__ __forceinline__ void wait_quietly(uint32_t bar, uint32_t parity) {
+  const unsigned long long t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < 1000000ull) {
+  }
+}
+
 template <bool E4M3>
 __host__ __device__ constexpr int chunk_threads() { return E4M3 ? 512 : 384; }
+
+// Shared memory: two Q tiles, the ring, and for e4m3 a slot of K's codes and one of V's.
+template <int D, bool E4M3>
+struct ChunkSmem {
+  static constexpr int NS = E4M3 ? 4 : D == 128 ? 5 : 8;
+  static constexpr int kTileBytes = kWTile * D * 2;
+  static constexpr int kOffQ = 0, kOffKv = 2 * kTileBytes;
+  static constexpr int kOffCode = kOffKv + NS * kTileBytes;
+  static constexpr int kOffExp = kOffCode + (E4M3 ? kTileBytes : 0);  // [2][128]
+  static constexpr int kOffMask = kOffExp + (E4M3 ? 256 : 0);         // [2]
+  static constexpr int kOffBar = kOffMask + 16;
+  static constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarKvFull = 2, kBarKvEmpty = 2 + NS, kBarS = 2 + 2 * NS,
+                       kBarP = 4 + 2 * NS, kBarP2 = 6 + 2 * NS, kBarO = 8 + 2 * NS, kBarOFree = 10 + 2 * NS,
+                       kBarDrain = 12 + 2 * NS, kBarCodeFull = 13 + 2 * NS, kBarCodeEmpty = 15 + 2 * NS;
+  static constexpr int kNumBars = 17 + 2 * NS;
+  static constexpr int kOffTmem = kOffBar + kNumBars * 8;
+  static constexpr int kBytes = kOffTmem + 16 + 1024;
+  static_assert(kBytes <= 227 * 1024);
+};
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
     cache_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const CacheAttnParams p) {
-  using L = WSmem<D>;
+  using L = ChunkSmem<D, E4M3>;
   constexpr int NS = L::NS, KT = kWTile;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -43,11 +70,12 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sgen + L::kOffTmem);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + L::kOffTmem + 4);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  volatile uint32_t* code_mask = reinterpret_cast<volatile uint32_t*>(sgen + L::kOffMask);  // boxes that exist
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
       const bool rows = (i >= L::kBarP && i < L::kBarP + 4) || (i >= L::kBarOFree && i < L::kBarOFree + 2);
-      const bool conv = E4M3 && i >= L::kBarKvFull && i < L::kBarKvFull + NS;
+      const bool conv = E4M3 && ((i >= L::kBarKvFull && i < L::kBarKvFull + NS) || i >= L::kBarCodeEmpty);
       mbar_init(bar(i), rows || conv ? 128 : 1);
     }
     *abort_flag = 0;
@@ -74,7 +102,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
   int64_t left = end - start;
   auto few_registers = [] {
     if (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
   };
   // Ends a piece of an item; false when the run is done.
   auto advance = [&](int stop) {
@@ -83,67 +111,94 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
     return left > 0 && it.next(p);
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ producers: Q and K, V
     few_registers();
-    uint32_t n = 0, nq = 0;
+    const bool is_v = warp == 2;
+    const CUtensorMap* tm = is_v ? &tmV : &tmK;
+    const uint8_t* exps = is_v ? p.c.v_exp : p.c.k_exp;
+    const int box_shift = min(p.c.page_shift, 6), boxes = KT >> box_shift;
+    uint32_t n = is_v, nq = 0;  // ring order K(0), V(0), K(1), ...
     bool ok = true;
     if (work) do {
-      const int stop = (int)min((int64_t)it.T, at + left);
-      ok = nq == 0 || role_wait(bar(L::kBarQEmpty), (nq - 1) & 1, kErrCcQEmpty, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar(L::kBarQFull), 2 * (D / 64) * tq * p.G * 128);
-        for (int h = 0; h < 2; ++h)
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(sQ + h * L::kTileBytes + c * (kWTile * 128), &tmQ, bar(L::kBarQFull), c * 64, 0,
-                        it.cu + it.tile * p.tpt + h * tq, it.hk);
+      const int stop = (int)min((int64_t)it.T, at + left), len = it.len();
+      if (!is_v) {
+        ok = nq == 0 || role_wait(bar(L::kBarQEmpty), (nq - 1) & 1, kErrCcQEmpty, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(L::kBarQFull), 2 * (D / 64) * tq * p.G * 128);
+          for (int h = 0; h < 2; ++h)
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_4d(sQ + h * L::kTileBytes + c * (kWTile * 128), &tmQ, bar(L::kBarQFull), c * 64, 0,
+                          it.cu + it.tile * p.tpt + h * tq, it.hk);
+        }
+        ++nq;
       }
-      ++nq;
-      if (!E4M3) {
-        const int box_shift = min(p.c.page_shift, 6), boxes = KT >> box_shift, len = it.len();
-        PageAhead<KT> pages;
-        pages.start(p, it, at, stop, lane);
-        for (int t = 2 * at; ok && t < 2 * stop; ++t, ++n) {  // K(0), V(0), K(1), V(1), ...
-          const int slot = n % NS, key0 = it.kt.key0(t >> 1);
-          const int pos = key0 + (lane << box_shift);
-          int64_t row = pages.get(p, it, t >> 1, lane);
-          if (lane >= boxes) row = -1;
+      PageAhead<KT> pages;
+      pages.start(p, it, at, stop, lane);
+      for (int t = at; t < stop; ++t, n += 2) {
+        const int key0 = it.kt.key0(t), pos = key0 + (lane << box_shift);
+        int64_t row = pages.get(p, it, t, lane);
+        if (lane >= boxes) row = -1;
+        const unsigned there = __ballot_sync(0xffffffffu, row >= 0);
+        const int place = pos & ((1 << p.c.page_shift) - 1);
+        const int64_t head = row + ((int64_t)it.hk << p.c.page_shift);
+        const int z = (int)((head - place) >> p.c.page_shift);
+        if (E4M3) {
+          const uint32_t full = bar(L::kBarCodeFull + is_v);
+          ok = n < 2 || role_wait(bar(L::kBarCodeEmpty + is_v), (n / 2 - 1) & 1, kErrCcKvEmpty, abort_flag);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) {
+            code_mask[is_v] = there;
+            mbar_arrive_expect_tx(full, ((uint32_t)__popc(there) << box_shift) * (D + 1));
+          }
+          __syncwarp();
+          if (row >= 0) {
+            tma_load_3d(sbase + L::kOffCode + is_v * (kWTile * D) + (lane << box_shift) * D, tm, full, 0, place, z);
+            bulk_load(sbase + L::kOffExp + is_v * 128 + (lane << box_shift), exps + head, 1u << box_shift, full);
+          }
+        } else {
+          const int slot = n % NS;
+          const uint32_t full = bar(L::kBarKvFull + slot), dst = sKv + slot * L::kTileBytes;
           ok = n < NS || role_wait(bar(L::kBarKvEmpty + slot), (n / NS - 1) & 1, kErrCcKvEmpty, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const uint32_t dst = sKv + slot * L::kTileBytes;
-          const unsigned there = __ballot_sync(0xffffffffu, row >= 0);
           if (key0 + KT > len || __popc(there) < boxes) {
-            const __nv_bfloat16* base = reinterpret_cast<const __nv_bfloat16*>((t & 1) ? p.c.v : p.c.k);
+            const __nv_bfloat16* base = reinterpret_cast<const __nv_bfloat16*>(is_v ? p.c.v : p.c.k);
             copy_tile<D>(dst, lane, [&](int r) -> const __nv_bfloat16* {
               const int64_t x = key0 + r < len ? cache_row(p.c, it.b, key0 + r) : -1;
               return x < 0 ? nullptr : base + (x + ((int64_t)it.hk << p.c.page_shift)) * D;
             });
-            if (lane == 0) mbar_arrive(bar(L::kBarKvFull + slot));
+            if (lane == 0) mbar_arrive(full);
           } else {
-            if (lane == 0) mbar_arrive_expect_tx(bar(L::kBarKvFull + slot), L::kTileBytes);
+            if (lane == 0) mbar_arrive_expect_tx(full, L::kTileBytes);
             __syncwarp();
-            if (lane < boxes) {
-              const int place = pos & ((1 << p.c.page_shift) - 1);
-              const int z = (int)((row - place + ((int64_t)it.hk << p.c.page_shift)) >> p.c.page_shift);
+            if (lane < boxes)
               for (int c = 0; c < D / 64; ++c)
-                tma_load_3d(dst + c * (KT * 128) + (lane << box_shift) * 128, (t & 1) ? &tmV : &tmK,
-                            bar(L::kBarKvFull + slot), c * 64, place, z);
-            }
+                tma_load_3d(dst + c * (KT * 128) + (lane << box_shift) * 128, tm, full, c * 64, place, z);
           }
-          __syncwarp();
         }
+        __syncwarp();
       }
       if (!ok || !advance(stop)) break;
     } while (true);
     // Never leave with copies in flight.
     if (lane == 0) {
       if (nq) mbar_wait(bar(L::kBarQFull), (nq - 1) & 1, kErrCcQ);
-      if (!E4M3)
-        for (uint32_t i = n > NS ? n - NS : 0; i < n; ++i)
-          mbar_wait(bar(L::kBarKvFull + i % NS), (i / NS) & 1, kErrCcKvFull);
+      if (E4M3) {
+        if (n >= 2) mbar_wait(bar(L::kBarCodeFull + is_v), (n / 2 - 1) & 1, kErrCcKvFull);
+      } else {
+        // Its loads that no later one has followed into their slot: where one
+        // has (the other warp's, the ring being odd), the slot was empty again.
+        // When a role gave up that is not known: each wait gets a millisecond.
+        const int last = (int)n - (is_v ? 2 : 1);  // the ring's last index
+        for (int i = max((int)n - 2 * (NS + 1), (int)is_v); i < (int)n; i += 2) {
+          if (ok && i + NS > last) mbar_wait(bar(L::kBarKvFull + i % NS), (i / NS) & 1, kErrCcKvFull);
+          else if (!ok) wait_quietly(bar(L::kBarKvFull + i % NS), (i / NS) & 1);
+        }
+      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -157,7 +212,8 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
     auto wait = [&](int b, uint32_t parity, unsigned int site) {
       return __all_sync(0xffffffffu, role_wait(bar(b), parity, site, abort_flag));
     };
-    uint32_t n = 0, nq = 0, np = 0;
+    uint32_t n = 0, nq = 0;
+    uint32_t steps[2] = {0, 0}, items[2] = {0, 0};  // of each tile
     bool ok = true;
     auto issue_s = [&](int x, int slot) {
       if (leader) {
@@ -173,24 +229,27 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
     };
     if (work) do {
       const int stop = (int)min((int64_t)it.T, at + left), total = stop - at;
+      const int nx = it.n - it.tile * p.tpt > tq ? 2 : 1;  // tile B may have no rows
       ok = wait(L::kBarQFull, nq & 1, kErrCcQ) && wait(L::kBarKvFull + n % NS, (n / NS) & 1, kErrCcKvFull);
       if (!ok) break;
       tc_fence_after();
       issue_s(0, n % NS);
-      issue_s(1, n % NS);
+      if (nx == 2) issue_s(1, n % NS);
       if (leader) {
         mma_commit(bar(L::kBarKvEmpty + n % NS));
         if (total == 1) mma_commit(bar(L::kBarQEmpty));
       }
       __syncwarp();
       ++n;
-      for (int t = 0; ok && t < total; ++t, ++np) {
+      for (int t = 0; ok && t < total; ++t) {
         const int vs = n % NS, ks = (n + 1) % NS;
         const bool more = t + 1 < total;
+#pragma unroll
         for (int x = 0; x < 2; ++x) {
+          if (x >= nx) break;
           if (x == 0) ok = wait(L::kBarKvFull + vs, (n / NS) & 1, kErrCcKvFull);
-          if (ok && t == 0 && nq > 0) ok = wait(L::kBarOFree + x, (nq - 1) & 1, kErrCcOFree);
-          ok = ok && wait(L::kBarP + x, np & 1, kErrCcP);
+          if (ok && t == 0 && items[x] > 0) ok = wait(L::kBarOFree + x, (items[x] - 1) & 1, kErrCcOFree);
+          ok = ok && wait(L::kBarP + x, steps[x] & 1, kErrCcP);
           if (!ok) break;
           tc_fence_after();
           if (leader) {
@@ -200,7 +259,8 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
               mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, v + kk * 128, idO, (t > 0 || kk > 0) ? 1u : 0u);
           }
           __syncwarp();
-          ok = wait(L::kBarP2 + x, np & 1, kErrCcP);
+          ok = wait(L::kBarP2 + x, steps[x] & 1, kErrCcP);
+          ++steps[x];
           if (!ok) break;
           tc_fence_after();
           if (leader) {
@@ -208,7 +268,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
 #pragma unroll
             for (int kk = kWTile / 32; kk < kWTile / 16; ++kk)
               mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, v + kk * 128, idO, 1u);
-            if (x == 1) mma_commit(bar(L::kBarKvEmpty + vs));
+            if (x == nx - 1) mma_commit(bar(L::kBarKvEmpty + vs));
             if (!more) mma_commit(bar(L::kBarO + x));
           }
           __syncwarp();
@@ -217,7 +277,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
             if (!ok) break;
             tc_fence_after();
             issue_s(x, ks);
-            if (x == 1 && leader) {
+            if (x == nx - 1 && leader) {
               mma_commit(bar(L::kBarKvEmpty + ks));
               if (t + 2 == total) mma_commit(bar(L::kBarQEmpty));
             }
@@ -227,6 +287,8 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
         n += more ? 2 : 1;
       }
       ++nq;
+      ++items[0];
+      if (nx == 2) ++items[1];
       if (!ok || !advance(stop)) break;
     } while (true);
     if (leader) mma_commit(bar(L::kBarDrain));
@@ -235,7 +297,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
   } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------ softmax and epilogue
     if (E4M3) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int x = (warp - 4) / 4;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -245,6 +307,10 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
     if (work) do {
       const int at0 = at, stop = (int)min((int64_t)it.T, at + left), len = it.len();
       const int64_t unit0 = end - left - at;
+      if (x == 1 && it.n - it.tile * p.tpt <= tq) {  // no rows here
+        if (!advance(stop)) break;
+        continue;
+      }
       const int tok = it.tile * p.tpt + x * tq + r / p.G;
       const bool live = r < tq * p.G && tok < it.n;
       const int i = it.first + min(tok, it.n - 1);
@@ -262,10 +328,6 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
         const int key0 = it.kt.key0(t);
         const unsigned m = __ballot_sync(0xffffffffu, next_absent);
         next_absent = absent(t + 1);
-        uint32_t gone[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          gone[c] = ((m >> (2 * c)) & 1u ? 0xFFFFu : 0u) | ((m >> (2 * c + 1)) & 1u ? 0xFFFF0000u : 0u);
         ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarS + x), np & 1, kErrCcS, abort_flag));
         if (!ok) break;
         tc_fence_after();
@@ -274,7 +336,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
                            (sink ? key0 + KT <= min(it.kt.cut, all_hi) : key0 >= all_lo && key0 + KT <= all_hi);
         const int e = (sink ? min(hi, it.kt.cut) : hi) - key0;
         softmax_tile<D>(ts, to, t == at, whole, sink ? 0 : lo - key0, e, p.w.sinks - key0, p.scale_log2, m_run, l_run,
-                        gone, [&] {
+                        m, [&] {
                           tc_fence_before();
                           mbar_arrive(bar(L::kBarP + x));
                         });
@@ -320,30 +382,27 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
     constexpr int RS = 128 / CH;           // rows between a thread's pieces
     uint32_t n = 0;
     bool ok = true;
-    uint4 code[N];
-    uint32_t power[N];  // bf16 2^e twice; 0 where the place does not exist
-    auto fetch = [&](int t) {
-      const int key0 = it.kt.key0(t >> 1), len = it.len();
-      const uint8_t *src = (t & 1) ? p.c.v : p.c.k, *ex = (t & 1) ? p.c.v_exp : p.c.k_exp;
+    if (work) do {
+      const int stop = (int)min((int64_t)it.T, at + left), len = it.len();
+      const int box_shift = min(p.c.page_shift, 6);
+      for (int t = 2 * at; ok && t < 2 * stop; ++t, ++n) {
+        const int slot = n % NS, is_v = t & 1, key0 = it.kt.key0(t >> 1);
+        ok = role_wait(bar(L::kBarCodeFull + is_v), (n / 2) & 1, kErrCcKvFull, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t there = code_mask[is_v], src = sbase + L::kOffCode + is_v * (kWTile * D);
+        uint4 code[N];
+        uint32_t power[N];  // 2^e as bf16, twice; 0 where the place does not exist
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int j = key0 + r0 + k * RS;
-        int64_t row = j < len ? cache_row(p.c, it.b, j) : -1;
-        code[k] = make_uint4(0, 0, 0, 0);
-        power[k] = 0;
-        if (row >= 0) {
-          row += (int64_t)it.hk << p.c.page_shift;
-          code[k] = *reinterpret_cast<const uint4*>(src + row * D + c * 16);
-          const uint32_t e = __ldg(ex + row);
-          power[k] = (e == 255 ? 0x7FC0u : e << 7) * 0x10001u;
+        for (int k = 0; k < N; ++k) {
+          const int r = r0 + k * RS;
+          const bool here = key0 + r < len && (there >> (r >> box_shift) & 1u);
+          const uint4 v = lds128(src + r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) * 16));
+          const uint32_t e = lds_u8(sbase + L::kOffExp + is_v * 128 + r);
+          code[k] = here ? v : make_uint4(0, 0, 0, 0);
+          power[k] = here ? (e == 255 ? 0x7FC0u : e << 7) * 0x10001u : 0u;
         }
-      }
-    };
-    if (work) {
-      int stop = (int)min((int64_t)it.T, at + left), t = 2 * at;
-      fetch(t);
-      while (true) {
-        const int slot = n % NS;
+        mbar_arrive(bar(L::kBarCodeEmpty + is_v));
         ok = n < NS || role_wait(bar(L::kBarKvEmpty + slot), (n / NS - 1) & 1, kErrCcKvEmpty, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -369,15 +428,9 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
         }
         fence_async_smem();
         mbar_arrive(bar(L::kBarKvFull + slot));
-        ++n;
-        if (++t == 2 * stop) {
-          if (!advance(stop)) break;
-          stop = (int)min((int64_t)it.T, at + left);
-          t = 2 * at;
-        }
-        fetch(t);
       }
-    }
+      if (!ok || !advance(stop)) break;
+    } while (true);
   } else {
     few_registers();
   }

@@ -165,11 +165,11 @@ __device__ __forceinline__ float exp_store(const float (&s)[kWTile], uint32_t ts
 
 // One softmax step of a row: 128 scores at taddr -> P (bf16 pairs) over them.
 // [a, e): the row's window relative to the tile, k: its sinks relative to it;
-// `whole`: every key of the tile is visible to every row of the warp; gone:
-// bits of the keys that do not exist, or null.
+// `whole`: every key of the tile is visible to every row of the warp; gone: a
+// bit for each 16 keys that do not exist.
 template <int D, typename Half>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, bool first, bool whole, int a, int e, int k,
-                                             float scale_log2, float& m_run, float& l_run, const uint32_t* gone,
+                                             float scale_log2, float& m_run, float& l_run, uint32_t gone,
                                              Half half) {
   float s[kWTile];
   {
@@ -188,7 +188,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, bool firs
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       uint32_t seen = bits_below(e - 32 * c) & (~bits_below(a - 32 * c) | bits_below(k - 32 * c));
-      if (gone) seen &= ~gone[c];
+      seen &= ~(((gone >> (2 * c)) & 1u ? 0xFFFFu : 0u) | ((gone >> (2 * c + 1)) & 1u ? 0xFFFF0000u : 0u));
 #pragma unroll
       for (int j = 0; j < 32; ++j) s[32 * c + j] = (seen >> j) & 1u ? s[32 * c + j] : -INFINITY;
     }
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const bool whole = sink ? key0 + kWTile <= min(kt.cut, all_hi) : key0 >= all_lo && key0 + kWTile <= all_hi;
         const int e = (sink ? min(hi, kt.cut) : hi) - key0;
         softmax_tile<D>(ts, to, t == 0, whole, sink ? 0 : lo - key0, e, p.w.sinks - key0, p.scale_log2, m_run, l_run,
-                        nullptr, [&] {
+                        0, [&] {
                           tc_fence_before();
                           mbar_arrive(bar(L::kBarP + x));
                         });

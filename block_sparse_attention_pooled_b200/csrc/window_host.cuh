@@ -276,9 +276,9 @@ sparge_status launch_cache_attn(const sparge_cache* c, const CacheAttnParams& p,
   }
   CUtensorMap mq;
   if (!make_map_q(&mq, p, D, plan.tpt / 2)) return SPARGE_ERR_CUDA;
-  e = ensure_smem(cache_chunk_kernel<D, E4M3>, WSmem<D>::kBytes, 40 + (D == 64 ? 0 : 2) + (E4M3 ? 1 : 0));
+  e = ensure_smem(cache_chunk_kernel<D, E4M3>, ChunkSmem<D, E4M3>::kBytes, 40 + (D == 64 ? 0 : 2) + (E4M3 ? 1 : 0));
   if (e != cudaSuccess) return cuda_status(e);
-  cache_chunk_kernel<D, E4M3><<<p.ctas, chunk_threads<E4M3>(), WSmem<D>::kBytes, st>>>(mq, mk, mv, p);
+  cache_chunk_kernel<D, E4M3><<<p.ctas, chunk_threads<E4M3>(), ChunkSmem<D, E4M3>::kBytes, st>>>(mq, mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e);
   cache_combine_kernel<D, kWTile><<<join, 128, 0, st>>>(p, plan.rows);
