@@ -12,9 +12,14 @@
 // movmatrix, in registers.
 //   S^T = K Q^T (16 keys x 8 rows x 16 channels a step), O^T += V^T P^T.
 // e4m3: a lane takes 16 codes of a row at a time, which fixes the order of the
-// channels within a step (Q is read in the same order); a code becomes bf16 by
-// its bits (exponent and mantissa shifted into place, times 2^120), exactly;
-// K's power multiplies the scores, V's the probabilities.
+// channels within a step (Q is read in the same order). Every code is exact in
+// fp16, so these products are fp16's, with what does not fit its range kept
+// outside: a row of Q enters times the power of two that puts its largest
+// element at 2^14 (exact but below 2^-39 of that), a key's power joins its
+// score, and a value's power joins the exponent of its probability: with
+// x_j the score in log2 units and e_j the power of v_j, the running maximum is
+// that of x_j + e_j, P_j = 2^(x_j + e_j - M) <= 1, and the row sum takes
+// P_j 2^-e_j.
 #pragma once
 #include <cuda.h>
 #include <cstdint>
@@ -101,6 +106,21 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 codes in the low half -> fp16 pair.
+__device__ __forceinline__ uint32_t codes_to_f16(uint32_t u) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)u, __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 // Two e4m3 codes in the upper bytes of u's halves -> bf16 pair, exact: sign,
 // exponent and mantissa in place make the value times 2^-120.
@@ -219,6 +239,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
     left -= stop - at;
     // Q as operand B: rows 8 x + g, channels as the keys' operand has them.
     uint32_t q[R8][D / 16][2];
+    float unq[R8][2];  // e4m3: what undoes the scaling of the lane's accumulator rows
 #pragma unroll
     for (int x = 0; x < R8; ++x) {
       const int r = 8 * x + g;
@@ -234,6 +255,27 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
         } else {
           q[x][k][0] = *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * c);
           q[x][k][1] = *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * c + 8);
+        }
+      }
+      if (E4M3) {
+        uint32_t top = 0;  // the row's largest magnitude, as bf16 bits
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) top = max(top, max(q[x][k][h] & 0x7FFFu, (q[x][k][h] >> 16) & 0x7FFFu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int shift = min(14 - ((int)(top >> 7) - 127), 100);
+        const float f = __uint_as_float((uint32_t)(127 + shift) << 23);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            q[x][k][h] = pack_f16x2(__uint_as_float(q[x][k][h] << 16) * f, __uint_as_float(q[x][k][h] & 0xFFFF0000u) * f);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int sh = __shfl_sync(0xffffffffu, shift, 4 * (2 * c + y));
+          unq[x][y] = p.scale_log2 * __uint_as_float((uint32_t)(127 - sh) << 23);
         }
       }
     }
@@ -268,13 +310,15 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
       const uint32_t sk = sbase + slot * L::kStage, sv = sk + L::kTile, ex = sbase + L::kOffExp + slot * 128;
       const bool exists = mask == 0xFu && key0 + KT <= len;
       const bool whole = exists && (sink ? key0 + KT <= min(it.kt.cut, all_hi) : key0 >= all_lo && key0 + KT <= all_hi);
-      if (!E4M3 && !exists) {
+      if (!exists) {
         // Zeros in V's rows that do not exist: memory may hold NaN there, and 0 * NaN is not 0.
-        for (int e = lane; e < KT * (D / 8); e += 32) {
-          const int r = e / (D / 8), ch = e % (D / 8);
+        // (Each warp its own keys; a row's pieces all go, so their order does not matter.)
+        constexpr int PPR = L::kRowBytes / 16;
+        for (int e = lane; e < 16 * MT * PPR; e += 32) {
+          const int r = 16 * k16 + e / PPR, ch = e % PPR;
           if (key0 + r >= len || !(mask >> (r >> 4) & 1u))
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(sv + (ch / 8) * (KT * 128) + r * 128 +
-                                                                          (ch % 8) * 16),
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             E4M3 ? sv + r * D + ch * 16 : sv + (ch / 8) * (KT * 128) + r * 128 + (ch % 8) * 16),
                          "r"(0)
                          : "memory");
         }
@@ -301,11 +345,10 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t a[4] = {
-                  codes_to_bf16(__byte_perm(w[0][k], 0, 0x1404)), codes_to_bf16(__byte_perm(w[1][k], 0, 0x1404)),
-                  codes_to_bf16(__byte_perm(w[0][k], 0, 0x3424)), codes_to_bf16(__byte_perm(w[1][k], 0, 0x3424))};
+              const uint32_t a[4] = {codes_to_f16(w[0][k]), codes_to_f16(w[1][k]), codes_to_f16(w[0][k] >> 16),
+                                     codes_to_f16(w[1][k] >> 16)};
 #pragma unroll
-              for (int x = 0; x < R8; ++x) mma16816(s[mt][x], a, q[x][4 * j + k][0], q[x][4 * j + k][1]);
+              for (int x = 0; x < R8; ++x) mma16816_f16(s[mt][x], a, q[x][4 * j + k][0], q[x][4 * j + k][1]);
             }
           }
         } else {
@@ -320,21 +363,26 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
         }
       }
       // To log2 units; keys that a row does not see to -inf.
-      float pv[MT][2];  // e4m3: V's powers of the lane's keys
+      float unv[MT][2];  // e4m3: 2^-e_j of the lane's keys
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          float f = p.scale_log2;
+          float pk = 1.0f, ev = 0.0f;
           if (E4M3) {
             const int r = 16 * (k16 + mt) + g + 8 * z;
-            f *= exp_scale((uint8_t)lds_u8(ex + r));
-            pv[mt][z] = exp_scale((uint8_t)lds_u8(ex + 64 + r));
+            pk = exp_scale((uint8_t)lds_u8(ex + r));
+            const uint32_t b = lds_u8(ex + 64 + r);
+            ev = b == 255 ? __int_as_float(0x7FC00000) : (float)((int)b - 127);
+            unv[mt][z] = __uint_as_float((254u - b) << 23);
           }
 #pragma unroll
           for (int x = 0; x < R8; ++x)
 #pragma unroll
-            for (int y = 0; y < 2; ++y) s[mt][x][2 * z + y] *= f;
+            for (int y = 0; y < 2; ++y) {
+              float& v = s[mt][x][2 * z + y];
+              v = E4M3 ? fmaf(v * unq[x][y], pk, ev) : v * p.scale_log2;
+            }
         }
       if (!whole) {
         const int most = sink ? it.kt.cut : len;
@@ -387,16 +435,15 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
-              float e = ex2_approx(s[mt][x][2 * z + y] - ref);
-              l_run[x][y] += e;
-              if (E4M3) e = e > 0.0f ? e * pv[mt][z] : 0.0f;  // a masked key's power may be anything
+              const float e = ex2_approx(s[mt][x][2 * z + y] - ref);
+              l_run[x][y] += E4M3 && e > 0.0f ? e * unv[mt][z] : e;  // a masked key's power may be anything
               s[mt][x][2 * z + y] = e;
             }
         }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          b[mt][x][0] = movmatrix_t(pack_bf16x2(s[mt][x][0], s[mt][x][1]));
-          b[mt][x][1] = movmatrix_t(pack_bf16x2(s[mt][x][2], s[mt][x][3]));
+          b[mt][x][0] = movmatrix_t(E4M3 ? pack_f16x2(s[mt][x][0], s[mt][x][1]) : pack_bf16x2(s[mt][x][0], s[mt][x][1]));
+          b[mt][x][1] = movmatrix_t(E4M3 ? pack_f16x2(s[mt][x][2], s[mt][x][3]) : pack_bf16x2(s[mt][x][2], s[mt][x][3]));
         }
       }
       // O^T
@@ -422,14 +469,13 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
             uint32_t a[4];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              // byte h (then h + 1) of both keys' words, into the halves' upper bytes
-              const uint32_t u = __byte_perm(w[2 * y][i], w[2 * y + 1][i], h == 0 ? 0x4000 : 0x6020);
-              const uint32_t v = __byte_perm(w[2 * y][i], w[2 * y + 1][i], h == 0 ? 0x5010 : 0x7030);
-              a[2 * y] = codes_to_bf16(u);
-              a[2 * y + 1] = codes_to_bf16(v);
+              // bytes h and h + 1 of both keys' words, key by key
+              const uint32_t u = __byte_perm(w[2 * y][i], w[2 * y + 1][i], h == 0 ? 0x5140 : 0x7362);
+              a[2 * y] = codes_to_f16(u);
+              a[2 * y + 1] = codes_to_f16(u >> 16);
             }
 #pragma unroll
-            for (int x = 0; x < R8; ++x) mma16816(o[k][x], a, b[mt][x][0], b[mt][x][1]);
+            for (int x = 0; x < R8; ++x) mma16816_f16(o[k][x], a, b[mt][x][0], b[mt][x][1]);
           }
         } else {
 #pragma unroll
