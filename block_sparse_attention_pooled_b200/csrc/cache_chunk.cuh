@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
     const bool is_v = warp == 2;
     const CUtensorMap* tm = is_v ? &tmV : &tmK;
     const uint8_t* exps = is_v ? p.c.v_exp : p.c.k_exp;
-    const int box_shift = min(p.c.page_shift, 6), boxes = KT >> box_shift;
+    const int box_shift = p.box_shift, boxes = KT >> box_shift;
     uint32_t n = is_v, nq = 0;  // ring order K(0), V(0), K(1), ...
     bool ok = true;
     if (work) do {
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
     bool ok = true;
     if (work) do {
       const int stop = (int)min((int64_t)it.T, at + left), len = it.len();
-      const int box_shift = min(p.c.page_shift, 6);
+      const int box_shift = p.box_shift;
       for (int t = 2 * at; ok && t < 2 * stop; ++t, ++n) {
         const int slot = n % NS, is_v = t & 1, key0 = it.kt.key0(t >> 1);
         ok = role_wait(bar(L::kBarCodeFull + is_v), (n / 2) & 1, kErrCcKvFull, abort_flag);

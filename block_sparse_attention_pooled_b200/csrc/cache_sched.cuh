@@ -48,6 +48,7 @@ struct CacheAttnParams {
   float2* part_ml;  // [2 * CTAs][rows]: reference (log2) and sum
   int H, G;
   int tpt;          // tokens per row tile
+  int box_shift;    // log2 of the keys in one TMA box of pages
   int ctas;         // CTAs that the units are dealt to
   float scale_log2;
 };
@@ -197,7 +198,7 @@ struct PageAhead {
   __device__ __forceinline__ int tiles() const { return 32 >> boxes_shift; }
   // Tiles at .. end - 1 of the item.
   __device__ __forceinline__ void start(const CacheAttnParams& p, const CacheItem<KT>& it, int at, int end, int lane) {
-    box_shift = min(p.c.page_shift, 6);
+    box_shift = p.box_shift;
     boxes_shift = 31 - __clz(KT) - box_shift;
     base = at;
     stop = end;

@@ -222,9 +222,11 @@ AttnPlan attn_plan(const sparge_cache* c, const sparge_cache_batch* b, int32_t H
   return a;
 }
 
-// Pages [pages * Hkv][page][d] with boxes of a page's rows (64 at most): bf16
-// in 64-column boxes with the 128-byte swizzle, codes in whole rows with the
-// swizzle of their width.
+// Pages [pages * Hkv][page][d] with boxes of a page's rows: bf16 in 64-column
+// boxes (64 rows at most) with the 128-byte swizzle, codes in whole rows with
+// the swizzle of their width.
+int box_rows(const sparge_cache* c) { return std::min(c->page, c->type == SPARGE_CACHE_E4M3 ? 128 : 64); }
+
 bool make_map_pages(CUtensorMap* m, const void* base, const sparge_cache* c) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
@@ -232,7 +234,7 @@ bool make_map_pages(CUtensorMap* m, const void* base, const sparge_cache* c) {
   const cuuint64_t width = q ? 1 : 2;
   cuuint64_t dims[3] = {(cuuint64_t)c->d, (cuuint64_t)c->page, (cuuint64_t)c->pages * c->Hkv};
   cuuint64_t strides[2] = {c->d * width, (cuuint64_t)c->page * c->d * width};
-  cuuint32_t box[3] = {q ? (cuuint32_t)c->d : 64, (cuuint32_t)std::min(c->page, 64), 1};
+  cuuint32_t box[3] = {q ? (cuuint32_t)c->d : 64, (cuuint32_t)box_rows(c), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, q ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -271,7 +273,7 @@ sparge_status launch_cache_attn(const sparge_cache* c, const CacheAttnParams& p,
   if (plan.rows <= 16) {
     e = plan.rows == 8 ? launch_decode<D, E4M3, 1>(mk, mv, p, st) : launch_decode<D, E4M3, 2>(mk, mv, p, st);
     if (e != cudaSuccess) return cuda_status(e);
-    cache_combine_kernel<D, kDecKeys><<<join, 128, 0, st>>>(p, plan.rows);
+    cache_combine_kernel<D, dec_keys<E4M3>()><<<join, 128, 0, st>>>(p, plan.rows);
     return cuda_status(cudaGetLastError());
   }
   CUtensorMap mq;
@@ -399,6 +401,8 @@ sparge_status sparge_cache_attn(const sparge_cache* cache, const sparge_cache_ba
   p.H = H;
   p.G = H / cache->Hkv;
   p.tpt = plan.tpt;
+  p.box_shift = 0;
+  while ((1 << p.box_shift) < box_rows(cache)) ++p.box_shift;
   p.ctas = plan.ctas;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)cache->d));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
