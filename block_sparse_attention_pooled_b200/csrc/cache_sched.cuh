@@ -1,5 +1,7 @@
 // How the work of attention over the paged cache is cut up. All lengths are in
-// device memory, so the kernels find their shares themselves.
+// device memory, so the kernels find their shares themselves, in a few
+// microseconds: that is most of a short call, so the walk keeps to 32 bits and
+// one round of loads where it can.
 //
 // An item is a row tile (up to `tpt` consecutive new tokens of a sequence,
 // times the G heads that share a K/V head) of one K/V head; its units are the
@@ -7,7 +9,8 @@
 // order (sequence, row tile, K/V head) are dealt to the CTAs in equal
 // contiguous runs: every CTA gets the same number of key tiles (to one),
 // however ragged the batch is. A run that ends inside an item leaves a partial
-// result; cache_combine_kernel joins an item's partials.
+// result; the CTA that has an item's first unit notes who holds the others
+// (`owners`), and cache_combine_kernel joins them.
 #pragma once
 #include <cstdint>
 
@@ -46,6 +49,7 @@ struct CacheAttnParams {
   float* lse;
   float* part_o;    // [2 * CTAs][rows][D]: a CTA's first and last partial
   float2* part_ml;  // [2 * CTAs][rows]: reference (log2) and sum
+  int2* owners;     // [tokens][Hkv]: first CTA of the token's item (bit 30: its last partial) and last CTA
   int H, G;
   int tpt;          // tokens per row tile
   int box_shift;    // log2 of the keys in one TMA box of pages
@@ -177,8 +181,14 @@ __device__ __forceinline__ CacheItem<KT> find_unit(const CacheAttnParams& p, int
     return true;
   });
   found.keys(p);
-  found.hk = (int)((u - base) / found.T);
-  at = (int)((u - base) % found.T);
+  const int64_t in = u - base;
+  if (in < INT32_MAX) {
+    found.hk = (int)in / found.T;
+    at = (int)in - found.hk * found.T;
+  } else {
+    found.hk = (int)(in / found.T);
+    at = (int)(in % found.T);
+  }
   return found;
 }
 
@@ -221,60 +231,52 @@ struct PageAhead {
 // up in more partials than tiles.
 __device__ __forceinline__ int ctas_used(int64_t W, int ctas) { return (int)max((int64_t)1, min((int64_t)ctas, W / 2)); }
 
-// CTA c's units: [c W / ctas, (c + 1) W / ctas).
-__device__ __forceinline__ int64_t run_start(int64_t W, int ctas, int c) { return W * c / ctas; }
+// CTA c's units: [c W / ctas, (c + 1) W / ctas); and the CTA that has unit u.
+__device__ __forceinline__ int64_t run_start(int64_t W, int ctas, int c) {
+  return W < (1 << 20) ? (int64_t)((uint32_t)W * (uint32_t)c / (uint32_t)ctas) : W * c / ctas;
+}
+__device__ __forceinline__ int run_owner(int64_t W, int ctas, int64_t u) {
+  return W < (1 << 20) ? (int)(((uint32_t)(u + 1) * (uint32_t)ctas - 1) / (uint32_t)W) : (int)(((u + 1) * ctas - 1) / W);
+}
 
-// One warp per (packed token, K/V head): joins the partials of the item that
-// the token's rows lie in, if any, head by head. ROWS: rows of a partial.
-template <int D, int KT>
+// One warp per (packed token, head): joins the partials of the item that the
+// token's rows lie in, if there is more than one. ROWS: rows of a partial.
+template <int D>
 __global__ void __launch_bounds__(128) cache_combine_kernel(const CacheAttnParams p, int rows) {
   constexpr int C = D / 32;
   const int lane = threadIdx.x % 32;
   const int64_t id = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-  const int t = (int)(id / p.c.Hkv), hk = (int)(id % p.c.Hkv);
+  const int t = (int)(id / p.H), h = (int)(id % p.H), hk = h / p.G;
   if (t >= min(__ldg(p.c.cu + p.c.B), p.c.tokens)) return;
-  const int64_t W = count_units<KT>(p, lane);
-  const int ctas = ctas_used(W, p.ctas);
-  // The units before the token's item.
-  const int b = find_seq(p.c.cu, p.c.B, t);
-  const int place = t - __ldg(p.c.cu + b), tile = place / p.tpt;
-  int64_t u0 = 0;
-  int T = 0;
-  walk_tiles<KT>(p, lane, [&](const CacheItem<KT>& x) {
-    const bool before = x.T > 0 && (x.b < b || (x.b == b && x.tile < tile));
-    if (before) u0 += x.T;
-    const unsigned here = __ballot_sync(0xffffffffu, x.T > 0 && x.b == b && x.tile == tile);
-    if (here) T = __shfl_sync(0xffffffffu, x.T, __ffs(here) - 1);
-    return here != 0;
-  });
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) u0 += __shfl_xor_sync(0xffffffffu, u0, o);
-  u0 = u0 * p.c.Hkv + (int64_t)hk * T;
-  const int c0 = (int)(((u0 + 1) * ctas - 1) / W), c1 = (int)(((u0 + T) * ctas - 1) / W);  // owners of the ends
+  const int2 own = p.owners[(int64_t)t * p.c.Hkv + hk];
+  const int c0 = own.x & 0x3FFFFFFF, c1 = own.y;
   if (c0 == c1) return;  // one CTA did it all
-  for (int g = 0; g < p.G; ++g) {
-    const int r = (place - tile * p.tpt) * p.G + g;
-    // A CTA's partial is its last one if the item starts in it, else its first.
-    auto slot = [&](int c) { return (int64_t)(2 * c + (run_start(W, ctas, c) < u0 ? 1 : 0)) * rows + r; };
-    float m = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[slot(c)].x);
+  const int place = t - __ldg(p.c.cu + find_seq(p.c.cu, p.c.B, t));
+  const int r = place % p.tpt * p.G + h % p.G;
+  auto slot = [&](int c) { return (int64_t)(2 * c + (c == c0 ? own.x >> 30 : 0)) * rows + r; };
+  float m = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[slot(c)].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.0f, o[C] = {};
-    for (int c = c0; c <= c1; ++c) {
-      const int64_t s = slot(c);
-      const float2 ml = p.part_ml[s];
-      if (!(ml.y > 0.0f) && ml.y == ml.y) continue;  // saw nothing
-      const float f = exp2f(ml.x - m);
-      l += ml.y * f;
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.0f, o[C] = {};
+  for (int b = c0; b <= c1; b += 32) {
+    const int n = min(32, c1 + 1 - b);
+    const float2 ml = lane < n ? p.part_ml[slot(b + lane)] : make_float2(0.0f, 0.0f);
+    const float f = ml.y == 0.0f ? 0.0f : exp2f(ml.x - m);  // 0: saw nothing
+    l += ml.y * f;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      const float* src = p.part_o + slot(b + i) * D + lane;
 #pragma unroll
-      for (int k = 0; k < C; ++k) o[k] += p.part_o[s * D + k * 32 + lane] * f;
+      for (int k = 0; k < C; ++k) o[k] += src[k * 32] * fi;
     }
-    const int64_t row = (int64_t)t * p.H + hk * p.G + g;
-#pragma unroll
-    for (int k = 0; k < C; ++k) p.O[row * D + k * 32 + lane] = __float2bfloat16_rn(l == 0.0f ? 0.0f : o[k] / l);
-    if (p.lse && lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
   }
+  l = warp_sum(l);
+  const int64_t row = (int64_t)t * p.H + h;
+#pragma unroll
+  for (int k = 0; k < C; ++k) p.O[row * D + k * 32 + lane] = __float2bfloat16_rn(l == 0.0f ? 0.0f : o[k] / l);
+  if (p.lse && lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace sparge

@@ -10,13 +10,15 @@ namespace sparge {
 // The row at position i sees [lo(i), hi(i, L)) and [0, min(sinks, hi)).
 struct Window {
   int left, right, sinks, unit;
+  __device__ __forceinline__ int unit_of(int i) const { return unit == 1 ? i : i / unit; }
   __device__ __forceinline__ int lo(int i) const {
-    const int f = i / unit - left;
-    return left < 0 || f <= 0 ? 0 : f * unit;
+    if (left < 0) return 0;
+    const int f = unit_of(i) - left;
+    return f <= 0 ? 0 : f * unit;
   }
   __device__ __forceinline__ int hi(int i, int L) const {
     if (right < 0) return L;
-    const long long e = ((long long)(i / unit) + right + 1) * unit;
+    const long long e = ((long long)unit_of(i) + right + 1) * unit;
     return e < L ? (int)e : L;
   }
 };

@@ -207,7 +207,7 @@ sparge_status check_cache(const sparge_cache* c, const sparge_cache_batch* b, Ca
 struct AttnPlan {
   int rows;  // 8, 16: cache_decode_kernel; 256: cache_chunk_kernel
   int tpt, ctas;
-  size_t bytes;
+  size_t owners, bytes;  // offset of the owners, and all
 };
 
 // Up to 16 rows a sequence the time is the cache's bytes and mma.sync keeps up
@@ -218,7 +218,8 @@ AttnPlan attn_plan(const sparge_cache* c, const sparge_cache_batch* b, int32_t H
   a.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 2 * kWTile;
   a.tpt = a.rows <= 16 ? (int)(a.rows / G) : (int)(kWTile / G) * 2;
   a.ctas = sm_count();
-  a.bytes = align256((size_t)2 * a.ctas * a.rows * 8) + align256((size_t)2 * a.ctas * a.rows * c->d * 4);
+  a.owners = align256((size_t)2 * a.ctas * a.rows * 8) + align256((size_t)2 * a.ctas * a.rows * c->d * 4);
+  a.bytes = a.owners + align256((size_t)b->tokens * c->Hkv * 8);
   return a;
 }
 
@@ -268,12 +269,12 @@ template <int D, bool E4M3>
 sparge_status launch_cache_attn(const sparge_cache* c, const CacheAttnParams& p, const AttnPlan& plan, cudaStream_t st) {
   CUtensorMap mk, mv;
   if (!make_map_pages(&mk, c->k, c) || !make_map_pages(&mv, c->v, c)) return SPARGE_ERR_CUDA;
-  const unsigned join = (unsigned)ceil_div((int64_t)p.c.tokens * p.c.Hkv, 4);
+  const unsigned join = (unsigned)ceil_div((int64_t)p.c.tokens * p.H, 4);
   cudaError_t e;
   if (plan.rows <= 16) {
     e = plan.rows == 8 ? launch_decode<D, E4M3, 1>(mk, mv, p, st) : launch_decode<D, E4M3, 2>(mk, mv, p, st);
     if (e != cudaSuccess) return cuda_status(e);
-    cache_combine_kernel<D, dec_keys<E4M3>()><<<join, 128, 0, st>>>(p, plan.rows);
+    cache_combine_kernel<D><<<join, 128, 0, st>>>(p, plan.rows);
     return cuda_status(cudaGetLastError());
   }
   CUtensorMap mq;
@@ -283,7 +284,7 @@ sparge_status launch_cache_attn(const sparge_cache* c, const CacheAttnParams& p,
   cache_chunk_kernel<D, E4M3><<<p.ctas, chunk_threads<E4M3>(), ChunkSmem<D, E4M3>::kBytes, st>>>(mq, mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e);
-  cache_combine_kernel<D, kWTile><<<join, 128, 0, st>>>(p, plan.rows);
+  cache_combine_kernel<D><<<join, 128, 0, st>>>(p, plan.rows);
   return cuda_status(cudaGetLastError());
 }
 
@@ -398,6 +399,7 @@ sparge_status sparge_cache_attn(const sparge_cache* cache, const sparge_cache_ba
   p.lse = lse;
   p.part_ml = static_cast<float2*>(workspace);
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256((size_t)2 * plan.ctas * plan.rows * 8));
+  p.owners = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + plan.owners);
   p.H = H;
   p.G = H / cache->Hkv;
   p.tpt = plan.tpt;
