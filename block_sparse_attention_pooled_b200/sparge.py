@@ -340,42 +340,34 @@ _pack_batch = struct.Struct("3P3i4x").pack
 _BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
 
 
-class _on:
-    """The stream to launch on (a raw handle) for tensors of `device`; makes that device current meanwhile."""
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+# The current stream's handle without an object for it.
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    __slots__ = ("handle", "guard", "foreign")
 
-    def __init__(self, device, stream):
-        index = device.index
-        current = torch.cuda.current_device()
-        if stream is None:
-            self.handle, self.foreign = torch.cuda.current_stream(index).cuda_stream, None
-        else:
-            if stream.device.index != index:
-                raise ValueError("the stream belongs to another device than the tensors")
-            self.handle = stream.cuda_stream
-            self.foreign = None if self.handle == torch.cuda.current_stream(index).cuda_stream else stream
-        self.guard = None if index == current else torch.cuda.device(index)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def keep(self, *tensors):
-        """Memory taken here for a stream that is not the current one is not handed out again before that stream is done."""
-        if self.foreign is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.foreign)
+def _launch(fn, args, device, stream, made):
+    """Calls fn(*args, stream handle) with the tensors' device current. `made`: tensors taken here; on a stream that is
+    not the current one, their memory is not handed out again before that stream is done with them."""
+    index = device.index
+    handle = _current_handle(index)
+    if stream is not None:
+        if stream.device.index != index:
+            raise ValueError("the stream belongs to another device than the tensors")
+        if stream.cuda_stream != handle:
+            handle = stream.cuda_stream
+            for t in made:
+                t.record_stream(stream)
+    if _get_device() == index:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, handle)
+    if rc:
+        raise SpargeError(rc, fn.__name__)
 
 
 def _want(t, name, dtype, shape, device):
-    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.get_device() != device.index or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}")
     return t.data_ptr()
 
@@ -395,31 +387,30 @@ def _window_args(Q, K, V, left, right, sinks, unit, lens):
 def sparge_window_fwd(Q, K, V, left: int, right: int, sinks: int = 0, unit: int = 1, lens=None, O=None, lse=None,
                       workspace=None, stream=None):
     """Attention with a sliding window and sinks over [B,H,N,d] (K, V: [B,Hkv,N,d]); left and right count units of
-    `unit` tokens, -1 for no limit; lens: int32 [B] lengths of a padded batch. Returns O (and fills lse if given)."""
+    `unit` tokens, -1 for no limit; lens: int32 [B] lengths of a padded batch. Returns O (and fills lse if given).
+    It needs no workspace."""
     shape, window, plens, _, device = _window_args(Q, K, V, left, right, sinks, unit, lens)
-    on = _on(device, stream)
+    made = ()
     if O is None:
         O = torch.empty_like(Q)
-        on.keep(O)
+        made = (O,)
     else:
         _want(O, "O", _BF16, Q.shape, device)
     plse = None if lse is None else _want(lse, "lse", _F32, Q.shape[:3], device)
-    ws, nws = _window_ws(OP_WINDOW_FWD, shape, window, workspace, device, on)
-    with on as handle:
-        rc = _lib.sparge_window_fwd(Q.data_ptr(), K.data_ptr(), V.data_ptr(), shape, window, plens, O.data_ptr(), plse,
-                                    ws, nws, handle)
-    _check(rc, "sparge_window_fwd")
+    _launch(_lib.sparge_window_fwd, (Q.data_ptr(), K.data_ptr(), V.data_ptr(), shape, window, plens, O.data_ptr(), plse,
+                                     None, 0), device, stream, made)
     return O
 
 
-def _window_ws(op, shape, window, workspace, device, on):
+def _space(workspace, n, device, made):
+    """Address and bytes of the workspace: the caller's, or n bytes taken here and added to `made`."""
     if workspace is None:
-        n = _lib.sparge_window_workspace_bytes(op, shape, window)
         if n == 0:
             return None, 0
         workspace = torch.empty(n, dtype=_U8, device=device)
-        on.keep(workspace)
-    elif workspace.device != device or not workspace.is_contiguous():
+        made.append(workspace)
+        return workspace.data_ptr(), n
+    if workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
@@ -428,10 +419,8 @@ def sparge_window_bwd(Q, K, V, O, lse, dO, left: int, right: int, sinks: int = 0
                       dK=None, dV=None, workspace=None, stream=None):
     """Gradients of sparge_window_fwd (O and lse from that call) for dL/dO = dO. Returns (dQ, dK, dV)."""
     shape, window, plens, kv, device = _window_args(Q, K, V, left, right, sinks, unit, lens)
-    for t, name in ((O, "O"), (dO, "dO")):
-        _want(t, name, _BF16, Q.shape, device)
+    pO, pdO = _want(O, "O", _BF16, Q.shape, device), _want(dO, "dO", _BF16, Q.shape, device)
     plse = _want(lse, "lse", _F32, Q.shape[:3], device)
-    on = _on(device, stream)
     made = []
     out = []
     for t, like, name in ((dQ, Q, "dQ"), (dK, K, "dK"), (dV, V, "dV")):
@@ -441,13 +430,11 @@ def sparge_window_bwd(Q, K, V, O, lse, dO, left: int, right: int, sinks: int = 0
         else:
             _want(t, name, _BF16, like.shape, device)
         out.append(t)
-    on.keep(*made)
-    ws, nws = _window_ws(OP_WINDOW_BWD, shape, window, workspace, device, on)
-    with on as handle:
-        rc = _lib.sparge_window_bwd(Q.data_ptr(), K.data_ptr(), V.data_ptr(), shape, window, plens, O.data_ptr(), plse,
-                                    dO.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws, nws,
-                                    handle)
-    _check(rc, "sparge_window_bwd")
+    n = _lib.sparge_window_workspace_bytes(OP_WINDOW_BWD, shape, window) if workspace is None else 0
+    ws, nws = _space(workspace, n, device, made)
+    _launch(_lib.sparge_window_bwd, (Q.data_ptr(), K.data_ptr(), V.data_ptr(), shape, window, plens, pO, plse, pdO,
+                                     out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws, nws), device, stream,
+            made)
     return tuple(out)
 
 
@@ -478,7 +465,7 @@ def _cache_args(k_pages, v_pages, k_exp, v_exp, page_table, first, cu, tokens):
 
 def _token_rows(t, name, heads, d, device):
     """Address and token stride of packed tokens [T, heads, d]: heads and channels contiguous, tokens any stride."""
-    if t.dtype != _BF16 or t.device != device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or (
+    if t.dtype is not _BF16 or t.get_device() != device.index or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or (
             t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d))):
         raise ValueError(f"{name} must be a bf16 tensor of shape [tokens, {heads}, {d}] on {device}, contiguous within a token")
     return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * d
@@ -492,9 +479,7 @@ def sparge_cache_write(k, v, k_pages, v_pages, page_table, first, cu_new, k_exp=
     pv, sv = _token_rows(v, "v", Hkv, d, device)
     if v.shape[0] != k.shape[0]:
         raise ValueError("k and v must hold the same tokens")
-    with _on(device, stream) as handle:
-        rc = _lib.sparge_cache_write(cache, batch, pk, sk, pv, sv, handle)
-    _check(rc, "sparge_cache_write")
+    _launch(_lib.sparge_cache_write, (cache, batch, pk, sk, pv, sv), device, stream, ())
 
 
 def sparge_cache_read(k_pages, v_pages, page_table, first, cu, tokens: int, k_exp=None, v_exp=None, K=None, V=None,
@@ -502,18 +487,16 @@ def sparge_cache_read(k_pages, v_pages, page_table, first, cu, tokens: int, k_ex
     """The batch's positions first[b], ... (cu[b+1] - cu[b] of them, `tokens` rows in all) as bf16 (K, V) [tokens,Hkv,d]."""
     cache, batch, device = _cache_args(k_pages, v_pages, k_exp, v_exp, page_table, first, cu, tokens)
     shape = (tokens, k_pages.shape[1], k_pages.shape[3])
-    on = _on(device, stream)
+    made = []
     out = []
     for t, name in ((K, "K"), (V, "V")):
         if t is None:
             t = torch.empty(shape, dtype=_BF16, device=device)
-            on.keep(t)
+            made.append(t)
         else:
             _want(t, name, _BF16, shape, device)
         out.append(t)
-    with on as handle:
-        rc = _lib.sparge_cache_read(cache, batch, out[0].data_ptr(), out[1].data_ptr(), handle)
-    _check(rc, "sparge_cache_read")
+    _launch(_lib.sparge_cache_read, (cache, batch, out[0].data_ptr(), out[1].data_ptr()), device, stream, made)
     return out[0], out[1]
 
 
@@ -526,24 +509,18 @@ def sparge_cache_attn(Q, k_pages, v_pages, page_table, first, cu_new, max_new: i
     T, H, d = Q.shape
     cache, batch, device = _cache_args(k_pages, v_pages, k_exp, v_exp, page_table, first, cu_new, T)
     pq, sq = _token_rows(Q, "Q", H, k_pages.shape[3], device)
-    on = _on(device, stream)
+    made = []
     if O is None:
         O = torch.empty((T, H, d), dtype=_BF16, device=device)
-        on.keep(O)
+        made.append(O)
     else:
         _want(O, "O", _BF16, Q.shape, device)
     plse = None if lse is None else _want(lse, "lse", _F32, (T, H), device)
     window = _pack_window(left, right, sinks, unit)
+    n = 0
     if workspace is None:
         n = _lib.sparge_cache_attn_workspace_bytes(cache, batch, H, max_new, max_len, window)
-        if n:
-            workspace = torch.empty(n, dtype=_U8, device=device)
-            on.keep(workspace)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    ws, nws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    with on as handle:
-        rc = _lib.sparge_cache_attn(cache, batch, pq, sq, H, max_new, max_len, window, O.data_ptr(), plse, ws, nws,
-                                    handle)
-    _check(rc, "sparge_cache_attn")
+    ws, nws = _space(workspace, n, device, made)
+    _launch(_lib.sparge_cache_attn, (cache, batch, pq, sq, H, max_new, max_len, window, O.data_ptr(), plse, ws, nws),
+            device, stream, made)
     return O
