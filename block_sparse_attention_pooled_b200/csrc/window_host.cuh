@@ -336,15 +336,15 @@ sparge_status sparge_cache_write(const sparge_cache* cache, const sparge_cache_b
   if (!all_aligned16({K, V}) || k_stride < least || v_stride < least || k_stride % 8 || v_stride % 8)
     return SPARGE_ERR_INVALID_ARG;
   const __nv_bfloat16 *k = static_cast<const __nv_bfloat16*>(K), *vv = static_cast<const __nv_bfloat16*>(V);
-  const unsigned grid = (unsigned)ceil_div((int64_t)batch->tokens * cache->Hkv * 2, 256 / (cache->d / 8));
+  const unsigned grid = (unsigned)ceil_div(batch->tokens, kCacheWarps);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool q = cache->type == SPARGE_CACHE_E4M3;
   if (cache->d == 64) {
-    if (q) cache_write_kernel<64, true><<<grid, 256, 0, s>>>(v, k, k_stride, vv, v_stride);
-    else cache_write_kernel<64, false><<<grid, 256, 0, s>>>(v, k, k_stride, vv, v_stride);
+    if (q) cache_write_kernel<64, true><<<grid, kCacheWarps * 32, 0, s>>>(v, k, k_stride, vv, v_stride);
+    else cache_write_kernel<64, false><<<grid, kCacheWarps * 32, 0, s>>>(v, k, k_stride, vv, v_stride);
   } else {
-    if (q) cache_write_kernel<128, true><<<grid, 256, 0, s>>>(v, k, k_stride, vv, v_stride);
-    else cache_write_kernel<128, false><<<grid, 256, 0, s>>>(v, k, k_stride, vv, v_stride);
+    if (q) cache_write_kernel<128, true><<<grid, kCacheWarps * 32, 0, s>>>(v, k, k_stride, vv, v_stride);
+    else cache_write_kernel<128, false><<<grid, kCacheWarps * 32, 0, s>>>(v, k, k_stride, vv, v_stride);
   }
   return cuda_status(cudaGetLastError());
 }
@@ -357,15 +357,15 @@ sparge_status sparge_cache_read(const sparge_cache* cache, const sparge_cache_ba
   if (batch->tokens == 0) return SPARGE_OK;
   if (!all_aligned16({K, V})) return SPARGE_ERR_INVALID_ARG;
   __nv_bfloat16 *k = static_cast<__nv_bfloat16*>(K), *vv = static_cast<__nv_bfloat16*>(V);
-  const unsigned grid = (unsigned)ceil_div((int64_t)batch->tokens * cache->Hkv * 2, 256 / (cache->d / 8));
+  const unsigned grid = (unsigned)ceil_div(batch->tokens, kCacheWarps);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool q = cache->type == SPARGE_CACHE_E4M3;
   if (cache->d == 64) {
-    if (q) cache_read_kernel<64, true><<<grid, 256, 0, s>>>(v, k, vv);
-    else cache_read_kernel<64, false><<<grid, 256, 0, s>>>(v, k, vv);
+    if (q) cache_read_kernel<64, true><<<grid, kCacheWarps * 32, 0, s>>>(v, k, vv);
+    else cache_read_kernel<64, false><<<grid, kCacheWarps * 32, 0, s>>>(v, k, vv);
   } else {
-    if (q) cache_read_kernel<128, true><<<grid, 256, 0, s>>>(v, k, vv);
-    else cache_read_kernel<128, false><<<grid, 256, 0, s>>>(v, k, vv);
+    if (q) cache_read_kernel<128, true><<<grid, kCacheWarps * 32, 0, s>>>(v, k, vv);
+    else cache_read_kernel<128, false><<<grid, kCacheWarps * 32, 0, s>>>(v, k, vv);
   }
   return cuda_status(cudaGetLastError());
 }
