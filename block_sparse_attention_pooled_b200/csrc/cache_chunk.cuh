@@ -7,8 +7,7 @@
 // tile holds 128 / G tokens and K and V are read once for the whole group. The
 // rows of Q come by a 4-D TMA box {64 channels, G heads, 128 / G tokens}.
 // K and V come by TMA, one box per page, from a warp each (a box costs its
-// issuing lane some hundred cycles). bf16: straight into the ring; a tile with
-// places that do not exist is copied by the warp's lanes, zeros there. e4m3:
+// issuing lane some hundred cycles). bf16: straight into the ring. e4m3:
 // the codes into a slot of their own, from where four more warps write them
 // into the ring as bf16, each times its row's power: exact.
 #pragma once
@@ -48,8 +47,9 @@ struct ChunkSmem {
   static constexpr int kOffBar = kOffMask + 16;
   static constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarKvFull = 2, kBarKvEmpty = 2 + NS, kBarS = 2 + 2 * NS,
                        kBarP = 4 + 2 * NS, kBarP2 = 6 + 2 * NS, kBarO = 8 + 2 * NS, kBarOFree = 10 + 2 * NS,
-                       kBarDrain = 12 + 2 * NS, kBarCodeFull = 13 + 2 * NS, kBarCodeEmpty = 15 + 2 * NS;
-  static constexpr int kNumBars = 17 + 2 * NS;
+                       kBarDrain = 12 + 2 * NS, kBarCodeFull = 13 + 2 * NS, kBarFix = 15 + 2 * NS,
+                       kBarCodeEmpty = 17 + 2 * NS;
+  static constexpr int kNumBars = 19 + 2 * NS;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffTmem + 16 + 1024;
   static_assert(kBytes <= 227 * 1024);
@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
     const uint8_t* exps = is_v ? p.c.v_exp : p.c.k_exp;
     const int box_shift = p.box_shift, boxes = KT >> box_shift;
     uint32_t n = is_v, nq = 0;  // ring order K(0), V(0), K(1), ...
+    FixUp fix{bar(L::kBarFix + is_v), 0};
     bool ok = true;
     if (work) do {
       const int stop = (int)min((int64_t)it.T, at + left), len = it.len();
@@ -165,19 +166,21 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
           ok = n < NS || role_wait(bar(L::kBarKvEmpty + slot), (n / NS - 1) & 1, kErrCcKvEmpty, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (key0 + KT > len || __popc(there) < boxes) {
-            const __nv_bfloat16* base = reinterpret_cast<const __nv_bfloat16*>(is_v ? p.c.v : p.c.k);
-            copy_tile<D>(dst, lane, [&](int r) -> const __nv_bfloat16* {
-              const int64_t x = key0 + r < len ? cache_row(p.c, it.b, key0 + r) : -1;
-              return x < 0 ? nullptr : base + (x + ((int64_t)it.hk << p.c.page_shift)) * D;
-            });
+          // A tile with places that do not exist lands on the warp's own barrier
+          // first and gets zeros there.
+          const bool broken = key0 + KT > len || __popc(there) < boxes;
+          const uint32_t land = broken ? fix.bar : full;
+          if (lane == 0) mbar_arrive_expect_tx(land, ((uint32_t)__popc(there) << box_shift) * (D * 2));
+          __syncwarp();
+          if (row >= 0)
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(dst + c * (KT * 128) + (lane << box_shift) * 128, tm, land, c * 64, place, z);
+          if (broken) {
+            ok = role_wait(fix.bar, fix.phase++ & 1, kErrCcKvFull, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            zero_rows<D>(dst, lane, [&](int r) { return key0 + r >= len || !(there >> (r >> box_shift) & 1u); });
             if (lane == 0) mbar_arrive(full);
-          } else {
-            if (lane == 0) mbar_arrive_expect_tx(full, L::kTileBytes);
-            __syncwarp();
-            if (lane < boxes)
-              for (int c = 0; c < D / 64; ++c)
-                tma_load_3d(dst + c * (KT * 128) + (lane << box_shift) * 128, tm, full, c * 64, place, z);
           }
         }
         __syncwarp();

@@ -9,9 +9,8 @@
 // sinks below the window, then the window. Roles:
 //   warp 0       producer: Q, then K and V tiles into a ring, by TMA; a tile
 //                that reaches past the sequence's end (or into a page that is
-//                not there) is copied by the warp's lanes, zeros in the rows
-//                that do not exist, so that what memory holds there never
-//                meets a probability of 0;
+//                not there) gets zeros in the rows that do not exist, so that
+//                what memory holds there never meets a probability of 0;
 //   warp 1       MMA issuer and TMEM owner;
 //   warps 4..7   softmax of tile A: one row (TMEM lane) per thread;
 //   warps 8..11  softmax of tile B.
@@ -36,7 +35,7 @@ namespace sparge {
 
 enum : unsigned int {
   kErrWinQ = 0x900, kErrWinQEmpty, kErrWinKvFull, kErrWinKvEmpty, kErrWinS, kErrWinP, kErrWinO, kErrWinOFree,
-  kErrWinDrain
+  kErrWinDrain, kErrWinFix
 };
 
 constexpr int kWTile = 128;       // rows per tile and keys per tile
@@ -47,7 +46,6 @@ struct WAttnParams {
   const int32_t* lens;  // whole sequences: [B] or null
   __nv_bfloat16* O;
   float* lse;
-  const __nv_bfloat16 *K, *V;  // for the tiles that the lanes copy
   int B, H, Hkv, N, items, rtiles;
   float scale_log2;
 };
@@ -61,38 +59,46 @@ struct WSmem {
   static constexpr int kOffBar = kOffKv + NS * kTileBytes;
   static constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarKvFull = 2, kBarKvEmpty = 2 + NS, kBarS = 2 + 2 * NS,
                        kBarP = 4 + 2 * NS, kBarP2 = 6 + 2 * NS, kBarO = 8 + 2 * NS, kBarOFree = 10 + 2 * NS,
-                       kBarDrain = 12 + 2 * NS;
-  static constexpr int kNumBars = 13 + 2 * NS;
+                       kBarDrain = 12 + 2 * NS, kBarFix = 13 + 2 * NS;
+  static constexpr int kNumBars = 14 + 2 * NS;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffTmem + 16 + 1024;
 };
 
-// Copies a [128 keys][D] tile (64-column boxes, 128-byte swizzle) by a warp's
-// lanes; row r comes from src(r), zeros where that is null.
-template <int D, typename Src>
-__device__ __forceinline__ void copy_tile(uint32_t dst, int lane, Src src) {
-  constexpr int CH = D / 8;         // 16-byte pieces per row
-  constexpr int RPI = 32 / CH;      // rows per step
+// Zeros in the rows of a [128][D] tile (64-column boxes, 128-byte swizzle) for
+// which bad(r), by a warp's lanes, after its loads have landed and before the
+// tensor core may read it: memory may hold NaN in places that no row sees, and
+// 0 * NaN is not 0. (Loading such a tile by the lanes instead took 12 us, 24
+// through a page table, which was most of a short call.)
+template <int D, typename Bad>
+__device__ __forceinline__ void zero_rows(uint32_t dst, int lane, Bad bad) {
+  constexpr int CH = D / 8;  // 16-byte pieces per row; a row's all go, so the swizzle does not matter
   const int c = lane % CH;
-  const uint32_t box = dst + (c / 8) * (kWTile * 128);
-#pragma unroll 1
-  for (int r0 = 0; r0 < kWTile; r0 += 4 * RPI) {
-    uint4 x[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const __nv_bfloat16* row = src(r0 + u * RPI + lane / CH);
-      x[u] = row ? *reinterpret_cast<const uint4*>(row + c * 8) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = r0 + u * RPI + lane / CH;
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + r * 128 + (((c % 8) ^ (r & 7)) * 16)),
-                   "r"(x[u].x), "r"(x[u].y), "r"(x[u].z), "r"(x[u].w)
-                   : "memory");
-    }
-  }
+  const uint32_t box = dst + (c / 8) * (kWTile * 128) + (c % 8) * 16;
+  for (int r = lane / CH; r < kWTile; r += 32 / CH)
+    if (bad(r)) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(box + r * 128), "r"(0) : "memory");
   fence_async_smem();
   __syncwarp();
+}
+
+// A producer warp's way to such tiles: their loads land on a barrier of its own.
+struct FixUp {
+  uint32_t bar;
+  uint32_t phase;
+};
+
+template <int D, typename Bad>
+__device__ __forceinline__ bool load_and_zero(uint32_t dst, const CUtensorMap* tm, int row0, int head, int lane, FixUp& fix,
+                                              volatile int* abort_flag, Bad bad) {
+  if (lane == 0) {
+    mbar_arrive_expect_tx(fix.bar, kWTile * D * 2);
+    for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * (kWTile * 128), tm, fix.bar, c * 64, row0, head);
+  }
+  const bool ok = role_wait(fix.bar, fix.phase & 1, kErrWinFix, abort_flag);
+  ++fix.phase;
+  if (!__all_sync(0xffffffffu, ok)) return false;
+  zero_rows<D>(dst, lane, bad);
+  return true;
 }
 
 using KeyTiles = KeyTilesT<kWTile>;
@@ -272,6 +278,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     // ------------------------------------------------------------ producer
     few_registers();
     uint32_t n = 0, nq = 0;  // ring slots filled, items with work
+    FixUp fix{bar(L::kBarFix), 0};
     bool ok = true;
     for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
       int bh, q0, len;
@@ -297,8 +304,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (!ok) break;
         const uint32_t dst = sKv + slot * L::kTileBytes;
         if (len < p.N && key0 + kWTile > len) {
-          const __nv_bfloat16* src = ((t & 1) ? p.V : p.K) + ((int64_t)kvh * p.N + key0) * D;
-          copy_tile<D>(dst, lane, [&](int r) { return key0 + r < len ? src + (int64_t)r * D : nullptr; });
+          ok = load_and_zero<D>(dst, (t & 1) ? &tmV : &tmK, key0, kvh, lane, fix, abort_flag,
+                                [&](int r) { return key0 + r >= len; });
+          if (!ok) break;
           if (lane == 0) mbar_arrive(bar(L::kBarKvFull + slot));
         } else if (lane == 0) {
           mbar_arrive_expect_tx(bar(L::kBarKvFull + slot), L::kTileBytes);

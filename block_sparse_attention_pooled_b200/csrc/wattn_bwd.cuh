@@ -10,8 +10,7 @@
 //   window_dkdv_kernel  one CTA per 128 keys (and part of the query tiles),
 //                       over the query tiles of all heads that share them.
 // Both: 128 x 128 score tiles (a 64-wide tile would be bound by the reads of
-// its operands from shared memory), warp 0 producer (TMA, or its lanes for a
-// tile that reaches past a sequence's end), warp 1 MMA issuer, warps 4..11 the
+// its operands from shared memory), warp 0 producer, warp 1 MMA issuer, warps 4..11 the
 // elementwise part: row = TMEM lane, warps 4..7 the tile's first 64 columns,
 // warps 8..11 the last.
 #pragma once
@@ -32,7 +31,7 @@ enum : unsigned int {
 struct WBwdParams {
   Window w;
   const int32_t* lens;
-  const __nv_bfloat16 *Q, *K, *V, *dO;
+  const __nv_bfloat16* dO;
   const float *lse, *dsum;
   __nv_bfloat16 *dQ, *dK, *dV;
   float* part;  // dK/dV of keys whose rows are split: [piece][2][128][D] fp32
@@ -54,19 +53,19 @@ __device__ __forceinline__ int key_row_hi(const Window& w, int j, int L) {
   return e < L ? (int)e : L;
 }
 
-// Loads a 128-row tile by TMA, or by the warp's lanes where it reaches past
-// the end of its sequence (len < N): zeros there, whatever memory holds.
+// Loads a 128-row tile; where it reaches past the end of its sequence
+// (len < N), zeros there, whatever memory holds.
 template <int D>
-__device__ __forceinline__ void load_rows(uint32_t dst, uint32_t bar, const CUtensorMap* tm,
-                                          const __nv_bfloat16* base, int row0, int len, int N, int head, int lane) {
+__device__ __forceinline__ bool load_rows(uint32_t dst, uint32_t bar, const CUtensorMap* tm, int row0, int len, int N,
+                                          int head, int lane, FixUp& fix, volatile int* abort_flag) {
   if (len < N && row0 + kWTile > len) {
-    const __nv_bfloat16* src = base + ((int64_t)head * N + row0) * D;
-    copy_tile<D>(dst, lane, [&](int r) { return row0 + r < len ? src + (int64_t)r * D : nullptr; });
+    if (!load_and_zero<D>(dst, tm, row0, head, lane, fix, abort_flag, [&](int r) { return row0 + r >= len; })) return false;
     if (lane == 0) mbar_arrive(bar);
   } else if (lane == 0) {
     mbar_arrive_expect_tx(bar, kWTile * D * 2);
     for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * (kWTile * 128), tm, bar, c * 64, row0, head);
   }
+  return true;
 }
 
 // D = A B^T over d, both operands [128][D] tiles, K-major.
@@ -117,8 +116,9 @@ struct WDqSmem {
   static constexpr int kOffQ = 0, kOffDO = kTileBytes, kOffKv = 2 * kTileBytes;
   static constexpr int kOffBar = kOffKv + NS * kTileBytes;
   static constexpr int kBarIn = 0, kBarFull = 1, kBarEmpty = 1 + NS, kBarS = 1 + 2 * NS, kBarDp = 3 + 2 * NS,
-                       kBarDpFree = 4 + 2 * NS, kBarDs = 5 + 2 * NS, kBarFinal = 6 + 2 * NS, kBarDrain = 7 + 2 * NS;
-  static constexpr int kNumBars = 8 + 2 * NS;
+                       kBarDpFree = 4 + 2 * NS, kBarDs = 5 + 2 * NS, kBarFinal = 6 + 2 * NS, kBarDrain = 7 + 2 * NS,
+                       kBarFix = 8 + 2 * NS;
+  static constexpr int kNumBars = 9 + 2 * NS;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffTmem + 16 + 1024;
 };
@@ -173,13 +173,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
           tma_load_3d(sDO + c * (kWTile * 128), &tmDO, bar(L::kBarIn), c * 64, q0, bh);
         }
       }
+      FixUp fix{bar(L::kBarFix), 0};
       int n = 0;
       for (; n < 2 * T; ++n) {  // K(0), V(0), K(1), ...
         const int slot = n % NS;
         const bool ok = n < NS || role_wait(bar(L::kBarEmpty + slot), (n / NS - 1) & 1, kErrWbEmpty, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) break;
-        load_rows<D>(sKv + slot * L::kTileBytes, bar(L::kBarFull + slot), (n & 1) ? &tmV : &tmK, (n & 1) ? p.V : p.K,
-                     kt.key0(n >> 1), len, p.N, kvh, lane);
+        if (!load_rows<D>(sKv + slot * L::kTileBytes, bar(L::kBarFull + slot), (n & 1) ? &tmV : &tmK, kt.key0(n >> 1),
+                          len, p.N, kvh, lane, fix, abort_flag))
+          break;
       }
       if (lane == 0) {
         mbar_wait(bar(L::kBarIn), 0, kErrWbIn);
@@ -327,8 +329,8 @@ struct WDkvSmem {
   static constexpr int kOffBar = kOffVec + 1024;
   static constexpr int kBarKV = 0, kBarFull = 1, kBarEmpty = 1 + NS, kBarS = 1 + 2 * NS, kBarDp = 2 + 2 * NS,
                        kBarP = 3 + 2 * NS, kBarDs = 4 + 2 * NS, kBarVecFull = 5 + 2 * NS, kBarVecEmpty = 7 + 2 * NS,
-                       kBarFinal = 9 + 2 * NS, kBarDrain = 10 + 2 * NS;
-  static constexpr int kNumBars = 11 + 2 * NS;
+                       kBarFinal = 9 + 2 * NS, kBarDrain = 10 + 2 * NS, kBarFix = 11 + 2 * NS;
+  static constexpr int kNumBars = 12 + 2 * NS;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffTmem + 16 + 1024;
   static_assert(kBytes <= 227 * 1024);
@@ -400,13 +402,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
           tma_load_3d(sV + c * (kWTile * 128), &tmV, bar(L::kBarKV), c * 64, k0, kvh);
         }
       }
+      FixUp fix{bar(L::kBarFix), 0};
       int n = 0, g = t0 / nq, qt = t0 % nq;
       for (; n < 2 * T; ++n) {  // Q(0), dO(0), Q(1), ...
         const int slot = n % NS;
         const bool ok = n < NS || role_wait(bar(L::kBarEmpty + slot), (n / NS - 1) & 1, kErrWbEmpty, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) break;
-        load_rows<D>(sRing + slot * L::kTileBytes, bar(L::kBarFull + slot), (n & 1) ? &tmDO : &tmQ,
-                     (n & 1) ? p.dO : p.Q, row0 + qt * kWTile, len, p.N, h0 + g, lane);
+        if (!load_rows<D>(sRing + slot * L::kTileBytes, bar(L::kBarFull + slot), (n & 1) ? &tmDO : &tmQ,
+                          row0 + qt * kWTile, len, p.N, h0 + g, lane, fix, abort_flag))
+          break;
         if ((n & 1) && ++qt == nq) qt = 0, ++g;
       }
       if (lane == 0) {

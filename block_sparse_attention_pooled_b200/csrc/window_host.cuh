@@ -99,8 +99,6 @@ sparge_status launch_window_fwd(const void* Q, const void* K, const void* V, con
   p.lens = lens;
   p.O = static_cast<__nv_bfloat16*>(O);
   p.lse = lse;
-  p.K = static_cast<const __nv_bfloat16*>(K);
-  p.V = static_cast<const __nv_bfloat16*>(V);
   p.B = s->B;
   p.H = s->H;
   p.Hkv = s->Hkv;
@@ -131,9 +129,6 @@ sparge_status launch_window_bwd(const void* Q, const void* K, const void* V, con
   WBwdParams p{};
   p.w = device_window(w);
   p.lens = lens;
-  p.Q = static_cast<const __nv_bfloat16*>(Q);
-  p.K = static_cast<const __nv_bfloat16*>(K);
-  p.V = static_cast<const __nv_bfloat16*>(V);
   p.dO = static_cast<const __nv_bfloat16*>(dO);
   p.lse = lse;
   p.dsum = dsum;
