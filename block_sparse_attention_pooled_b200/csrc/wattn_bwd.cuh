@@ -31,8 +31,9 @@ enum : unsigned int {
 struct WBwdParams {
   Window w;
   const int32_t* lens;
-  const __nv_bfloat16* dO;
-  const float *lse, *dsum;
+  const __nv_bfloat16 *O, *dO;
+  const float* lse;
+  float* dsum;  // [B,H,N] D_i
   __nv_bfloat16 *dQ, *dK, *dV;
   float* part;  // dK/dV of keys whose rows are split: [piece][2][128][D] fp32
   int B, H, Hkv, N;
@@ -114,7 +115,8 @@ struct WDqSmem {
   static constexpr int NS = D == 128 ? 5 : 8;
   static constexpr int kTileBytes = kWTile * D * 2;
   static constexpr int kOffQ = 0, kOffDO = kTileBytes, kOffKv = 2 * kTileBytes;
-  static constexpr int kOffBar = kOffKv + NS * kTileBytes;
+  static constexpr int kOffDot = kOffKv + NS * kTileBytes;  // [128] fp32
+  static constexpr int kOffBar = kOffDot + 512;
   static constexpr int kBarIn = 0, kBarFull = 1, kBarEmpty = 1 + NS, kBarS = 1 + 2 * NS, kBarDp = 3 + 2 * NS,
                        kBarDpFree = 4 + 2 * NS, kBarDs = 5 + 2 * NS, kBarFinal = 6 + 2 * NS, kBarDrain = 7 + 2 * NS,
                        kBarFix = 8 + 2 * NS;
@@ -246,7 +248,38 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
     const int64_t row = (int64_t)bh * p.N + i;
     const float nl2 = live ? -__ldg(p.lse + row) * 1.4426950408889634f : 0.0f;
-    const float nd = live ? -__ldg(p.dsum + row) : 0.0f;
+    // D_i in fp32, 16 rows per warp, a row's 16-byte pieces on neighbouring lanes.
+    float* dots = reinterpret_cast<float*>(sgen + L::kOffDot);
+    {
+      constexpr int LPR = D / 8, RPS = 32 / LPR, U = 16 / RPS;
+      const int r0 = (warp - 4) * 16 + lane / LPR;
+      const int64_t base = ((int64_t)bh * p.N + q0 + r0) * D + lane % LPR * 8;
+      uint4 a[U], g[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool in = q0 + r0 + u * RPS < len;
+        a[u] = in ? __ldg(reinterpret_cast<const uint4*>(p.O + base + u * RPS * D)) : make_uint4(0, 0, 0, 0);
+        g[u] = in ? __ldg(reinterpret_cast<const uint4*>(p.dO + base + u * RPS * D)) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t av[4] = {a[u].x, a[u].y, a[u].z, a[u].w}, gv[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
+        float dot = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          dot = fmaf(__uint_as_float(av[k] << 16), __uint_as_float(gv[k] << 16), dot);
+          dot = fmaf(__uint_as_float(av[k] & 0xFFFF0000u), __uint_as_float(gv[k] & 0xFFFF0000u), dot);
+        }
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane % LPR == 0) {
+          dots[r0 + u * RPS] = dot;
+          if (q0 + r0 + u * RPS < len) p.dsum[(int64_t)bh * p.N + q0 + r0 + u * RPS] = dot;
+        }
+      }
+    }
+    asm volatile("bar.sync 2, 256;" ::: "memory");
+    const float nd = -dots[r];
     const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), nl = f2(nl2, nl2), nd2 = f2(nd, nd);
     bool ok = true;
     for (int t = 0; t < T; ++t) {
@@ -320,6 +353,14 @@ __global__ void __launch_bounds__(kWThreads, 1)
 // has dK(t) and dP(t+1) to do, and while they form dS(t+1), dV(t+1) and S(t+2).
 // Warp 2 brings each query tile's lse and D.
 // ---------------------------------------------------------------------------
+// Where a piece's sums go, in units of [2][128][D]: the sinks' tiles first.
+__device__ __forceinline__ int64_t part_slot(const WBwdParams& p, int kvh, int tile, int piece) {
+  const int st = p.sink_tiles;
+  if (tile < st) return ((int64_t)kvh * st + tile) * p.sink_pieces + piece;
+  const int64_t sinks = p.sink_pieces > 1 ? (int64_t)p.B * p.Hkv * st * p.sink_pieces : 0;
+  return sinks + ((int64_t)kvh * (p.rtiles - st) + tile - st) * p.pieces + piece;
+}
+
 template <int D>
 struct WDkvSmem {
   static constexpr int NS = D == 128 ? 5 : 8;
@@ -583,9 +624,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const uint32_t acc = tmem + (wg == 0 ? 256 : 384) + lane_off;
     const float f = wg == 0 ? 1.0f : p.scale;
     if (pieces > 1) {
-      const int64_t slot = in_sink ? (int64_t)(kvh * p.sink_tiles + tile) * pieces + piece
-                                   : (int64_t)BHkv * nsink +
-                                         ((int64_t)kvh * (p.rtiles - p.sink_tiles) + tile - p.sink_tiles) * pieces + piece;
+      const int64_t slot = part_slot(p, kvh, tile, piece);
       float* out = p.part + ((slot * 2 + wg) * kWTile + r) * D;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
@@ -617,25 +656,25 @@ __global__ void __launch_bounds__(kWThreads, 1)
 }
 
 // dK, dV of the keys whose rows were split: the pieces added in order. One
-// thread per four channels of a (class tile, which, key).
+// thread per four channels of a (K/V head, tile, which, key).
 template <int D>
-__global__ void __launch_bounds__(256)
-    window_reduce_kernel(const float* __restrict__ part, int pieces, int tile0, int tiles, int N, int64_t quads,
-                         __nv_bfloat16* __restrict__ dK, __nv_bfloat16* __restrict__ dV) {
+__global__ void __launch_bounds__(256) window_reduce_kernel(const WBwdParams p, int64_t quads) {
   constexpr int QD = D / 4;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= quads) return;
   const int c = (int)(i % QD) * 4, r = (int)(i / QD % kWTile), which = (int)(i / QD / kWTile % 2);
-  const int64_t ct = i / QD / kWTile / 2;  // kvh * tiles + tile within the class
-  const int key = (tile0 + (int)(ct % tiles)) * kWTile + r;
-  if (key >= N) return;
-  const float* src = part + ((ct * pieces * 2 + which) * kWTile + r) * D + c;
+  const int ct = (int)(i / QD / kWTile / 2), kvh = ct / p.rtiles, tile = ct % p.rtiles;
+  const bool in_sink = tile < p.sink_tiles;
+  const int pieces = in_sink ? p.sink_pieces : p.pieces, key = tile * kWTile + r;
+  if (pieces <= 1 || key >= p.N) return;
+  const int64_t slot = part_slot(p, kvh, tile, 0);
+  const float* src = p.part + ((slot * 2 + which) * kWTile + r) * D + c;
   float4 a = *reinterpret_cast<const float4*>(src);
   for (int k = 1; k < pieces; ++k) {
     const float4 x = *reinterpret_cast<const float4*>(src + (int64_t)k * 2 * kWTile * D);
     a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
   }
-  __nv_bfloat16* out = (which == 0 ? dV : dK) + (ct / tiles * N + key) * D + c;
+  __nv_bfloat16* out = (which == 0 ? p.dV : p.dK) + ((int64_t)kvh * p.N + key) * D + c;
   *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
 }
 

@@ -56,8 +56,7 @@ KvSplit kv_split(const sparge_window_shape* s, const sparge_window* w, const WDi
   const int64_t most = std::max<int64_t>(8, all / (3 * 148));
   k.pieces = (int)std::min<int64_t>(ceil_div(run, most), 64);
   k.sink_pieces = (int)std::min<int64_t>(ceil_div(sink_run, most), 64);
-  const size_t sinks = (size_t)d.BHkv * k.sink_tiles * k.sink_pieces;
-  k.slots = (k.sink_tiles > 0 && k.sink_pieces > 1) || k.pieces > 1 ? sinks : 0;
+  k.slots = k.sink_pieces > 1 ? (size_t)d.BHkv * k.sink_tiles * k.sink_pieces : 0;
   if (k.pieces > 1) k.slots += (size_t)d.BHkv * (k.tiles - k.sink_tiles) * k.pieces;
   return k;
 }
@@ -124,14 +123,14 @@ sparge_status launch_window_bwd(const void* Q, const void* K, const void* V, con
       !make_map_bhnd(&mv, V, dm.BHkv, s->N, D, kWTile) || !make_map_bhnd(&mdo, dO, dm.BH, s->N, D, kWTile))
     return SPARGE_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  float* dsum = static_cast<float*>(workspace);
   const KvSplit k = kv_split(s, w, dm);
   WBwdParams p{};
   p.w = device_window(w);
   p.lens = lens;
+  p.O = static_cast<const __nv_bfloat16*>(O);
   p.dO = static_cast<const __nv_bfloat16*>(dO);
   p.lse = lse;
-  p.dsum = dsum;
+  p.dsum = static_cast<float*>(workspace);
   p.dQ = static_cast<__nv_bfloat16*>(dQ);
   p.dK = static_cast<__nv_bfloat16*>(dK);
   p.dV = static_cast<__nv_bfloat16*>(dV);
@@ -149,22 +148,16 @@ sparge_status launch_window_bwd(const void* Q, const void* K, const void* V, con
   const int64_t gq = dm.BH * k.tiles;
   const int64_t gk = dm.BHkv * ((int64_t)k.sink_tiles * k.sink_pieces + (int64_t)(k.tiles - k.sink_tiles) * k.pieces);
   if (gq > INT32_MAX || gk > INT32_MAX) return SPARGE_ERR_UNSUPPORTED;
-  bwd_dot_kernel<D><<<(unsigned)ceil_div(dm.rows, 256 / (D / 8)), 256, 0, st>>>(
-      static_cast<const __nv_bfloat16*>(O), p.dO, dm.rows, dsum);
   cudaError_t e = ensure_smem(window_dq_kernel<D>, WDqSmem<D>::kBytes, D == 64 ? 22 : 23);
   if (e != cudaSuccess) return cuda_status(e);
   window_dq_kernel<D><<<(unsigned)gq, kWThreads, WDqSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, p);
   e = ensure_smem(window_dkdv_kernel<D>, WDkvSmem<D>::kBytes, D == 64 ? 24 : 25);
   if (e != cudaSuccess) return cuda_status(e);
   window_dkdv_kernel<D><<<(unsigned)gk, kWThreads, WDkvSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, p);
-  for (int c = 0; c < 2; ++c) {
-    const int pieces = c == 0 ? k.sink_pieces : k.pieces, tile0 = c == 0 ? 0 : k.sink_tiles;
-    const int tiles = c == 0 ? k.sink_tiles : k.tiles - k.sink_tiles;
-    if (pieces <= 1 || tiles == 0) continue;
-    const float* part = p.part + (c == 0 ? 0 : (size_t)dm.BHkv * k.sink_tiles * k.sink_pieces * 2 * kWTile * D);
-    const int64_t quads = dm.BHkv * tiles * 2 * kWTile * (D / 4);
-    window_reduce_kernel<D><<<(unsigned)ceil_div(quads, 256), 256, 0, st>>>(part, pieces, tile0, tiles, s->N, quads,
-                                                                           p.dK, p.dV);
+  if (k.slots > 0) {
+    const int64_t quads = dm.BHkv * k.tiles * 2 * kWTile * (D / 4);
+    if (ceil_div(quads, 256) > INT32_MAX) return SPARGE_ERR_UNSUPPORTED;
+    window_reduce_kernel<D><<<(unsigned)ceil_div(quads, 256), 256, 0, st>>>(p, quads);
   }
   return cuda_status(cudaGetLastError());
 }
