@@ -80,6 +80,33 @@ __device__ __forceinline__ void mma_rows(uint32_t d_tmem, uint64_t a, uint64_t b
   }
 }
 
+// The same with A as bf16 pairs in TMEM (D / 2 columns).
+template <int D>
+__device__ __forceinline__ void mma_rows_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b) {
+  constexpr uint32_t id = idesc_bf16_f32(kWTile, kWTile, false, false);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    mma_ts(d_tmem, a_tmem + kk * 8, b + (((kk >> 2) * (kWTile * 128) + (kk & 3) * 32) >> 4), id, kk > 0 ? 1u : 0u);
+}
+
+// Row r of a [128][D] tile in shared memory (128-byte swizzle) into TMEM.
+template <int D>
+__device__ __forceinline__ void row_to_tmem(uint32_t tile, int r, uint32_t taddr) {
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t w[16];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int ch = 4 * c + k;
+      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[4 * k]), "=r"(w[4 * k + 1]), "=r"(w[4 * k + 2]), "=r"(w[4 * k + 3])
+                   : "r"(tile + (ch / 8) * (kWTile * 128) + r * 128 + (((ch % 8) ^ (r & 7)) * 16))
+                   : "memory");
+    }
+    tmem_st16(taddr + 16 * c, w);
+  }
+}
+
 // D (+)= A B over the tile's 128 columns: A bf16 pairs in TMEM, columns 0..63
 // of the tile at a_tmem, 64..127 at a_tmem + 64; B a [128][D] tile, MN-major.
 template <int D>
@@ -105,24 +132,28 @@ __device__ __forceinline__ void store_zero(__nv_bfloat16* out) {
 }
 
 // ---------------------------------------------------------------------------
-// dQ. TMEM columns: S(t) [0,128) and [128,256) in turn, dP [256,384), dQ
-// [384,384+D); dS(t) (bf16 pairs) over the columns of S(t). Issue order:
-// S(t+1); dP(t+1) once dP(t) is in registers; dQ += dS(t) K(t): the next
-// tile's scores are there when the warps finish this one's.
+// dQ. TMEM columns: S [0,128), dP [128,256), dQ [256,256+D), Q [384,384+D/2),
+// dO [448,448+D/2) (bf16 pairs); dS(t) (bf16 pairs) over dP(t). Q and dO are the
+// A operands of every tile's products: from TMEM they are not read from shared
+// memory again and again, whose bandwidth bounds this kernel (about 95 of 128
+// bytes a clock go through): 96 KB instead of 160 a tile, and their 64 KB become
+// ring slots. Issue order: S(t+1) once S(t) is in registers; dQ += dS(t) K(t);
+// dP(t+1). While the warps finish dS(t), S(t+1) runs; while they form P(t+1),
+// dQ(t) and dP(t+1) do.
 // ---------------------------------------------------------------------------
 template <int D>
 struct WDqSmem {
-  static constexpr int NS = D == 128 ? 5 : 8;
+  static constexpr int NS = D == 128 ? 7 : 10;
   static constexpr int kTileBytes = kWTile * D * 2;
-  static constexpr int kOffQ = 0, kOffDO = kTileBytes, kOffKv = 2 * kTileBytes;
-  static constexpr int kOffDot = kOffKv + NS * kTileBytes;  // [128] fp32
+  static constexpr int kOffDot = NS * kTileBytes;  // [128] fp32; Q and dO land in the last two slots first
   static constexpr int kOffBar = kOffDot + 512;
-  static constexpr int kBarIn = 0, kBarFull = 1, kBarEmpty = 1 + NS, kBarS = 1 + 2 * NS, kBarDp = 3 + 2 * NS,
-                       kBarDpFree = 4 + 2 * NS, kBarDs = 5 + 2 * NS, kBarFinal = 6 + 2 * NS, kBarDrain = 7 + 2 * NS,
-                       kBarFix = 8 + 2 * NS;
+  static constexpr int kBarIn = 0, kBarFull = 1, kBarEmpty = 1 + NS, kBarS = 1 + 2 * NS, kBarDp = 2 + 2 * NS,
+                       kBarSFree = 3 + 2 * NS, kBarDs = 4 + 2 * NS, kBarTaken = 5 + 2 * NS, kBarFinal = 6 + 2 * NS,
+                       kBarDrain = 7 + 2 * NS, kBarFix = 8 + 2 * NS;
   static constexpr int kNumBars = 9 + 2 * NS;
   static constexpr int kOffTmem = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffTmem + 16 + 1024;
+  static_assert(kBytes <= 227 * 1024);
 };
 
 template <int D>
@@ -136,7 +167,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - raw);
-  const uint32_t sQ = sbase + L::kOffQ, sDO = sbase + L::kOffDO, sKv = sbase + L::kOffKv;
+  const uint32_t sKv = sbase, sQ = sKv + (NS - 2) * L::kTileBytes, sDO = sQ + L::kTileBytes;
   auto bar = [&](int i) { return sbase + L::kOffBar + 8u * (uint32_t)i; };
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(sgen + L::kOffTmem);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + L::kOffTmem + 4);
@@ -151,7 +182,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   const int T = kt.total;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), i == L::kBarDpFree || i == L::kBarDs ? 256 : 1);
+    for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), i == L::kBarSFree || i == L::kBarDs || i == L::kBarTaken ? 256 : 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -179,7 +210,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
       int n = 0;
       for (; n < 2 * T; ++n) {  // K(0), V(0), K(1), ...
         const int slot = n % NS;
-        const bool ok = n < NS || role_wait(bar(L::kBarEmpty + slot), (n / NS - 1) & 1, kErrWbEmpty, abort_flag);
+        const bool ok = n == NS - 2 ? role_wait(bar(L::kBarTaken), 0, kErrWbIn, abort_flag)
+                                    : n < NS || role_wait(bar(L::kBarEmpty + slot), (n / NS - 1) & 1, kErrWbEmpty, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) break;
         if (!load_rows<D>(sKv + slot * L::kTileBytes, bar(L::kBarFull + slot), (n & 1) ? &tmV : &tmK, kt.key0(n >> 1),
                           len, p.N, kvh, lane, fix, abort_flag))
@@ -193,32 +225,23 @@ __global__ void __launch_bounds__(kWThreads, 1)
   } else if (warp == 1) {
     few_registers();
     const bool leader = elect_one();
-    const uint64_t dQ = sdesc_sw128(sQ, 16, 1024), dDO = sdesc_sw128(sDO, 16, 1024);
     const uint64_t dKv = sdesc_sw128(sKv, 16, 1024), dKvM = sdesc_sw128(sKv, kWTile * 128, 1024);
     auto wait = [&](int i, uint32_t parity, unsigned int site) {
       return __all_sync(0xffffffffu, role_wait(bar(i), parity, site, abort_flag));
     };
     auto slot = [&](int n) { return (uint64_t)(((n % NS) * L::kTileBytes) >> 4); };
-    bool ok = T > 0 && wait(L::kBarIn, 0, kErrWbIn);
+    auto full = [&](int n) { return wait(L::kBarFull + n % NS, (n / NS) & 1, kErrWbFull); };
+    bool ok = T > 0 && wait(L::kBarTaken, 0, kErrWbIn);
     for (int t = -1; ok && t < T; ++t) {
-      if (t + 1 < T) {
-        const int k = 2 * (t + 1), v = k + 1;
-        ok = wait(L::kBarFull + k % NS, (k / NS) & 1, kErrWbFull);
+      const bool more = t + 1 < T;
+      const int k = 2 * (t + 1), v = k + 1;
+      if (more) {
+        ok = full(k) && (t < 0 || wait(L::kBarSFree, t & 1, kErrWbS));
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-          mma_rows<D>(tmem + ((t + 1) & 1) * 128, dQ, dKv + slot(k));
-          mma_commit(bar(L::kBarS + ((t + 1) & 1)));
-        }
-        __syncwarp();
-        ok = wait(L::kBarFull + v % NS, (v / NS) & 1, kErrWbFull) &&
-             (t < 0 || wait(L::kBarDpFree, t & 1, kErrWbDpFree));
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          mma_rows<D>(tmem + 256, dDO, dKv + slot(v));
-          mma_commit(bar(L::kBarDp));
-          mma_commit(bar(L::kBarEmpty + v % NS));
+          mma_rows_ts<D>(tmem, tmem + 384, dKv + slot(k));
+          mma_commit(bar(L::kBarS));
         }
         __syncwarp();
       }
@@ -227,9 +250,20 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-          mma_cols<D>(tmem + 384, tmem + (t & 1) * 128, dKvM + slot(2 * t), t > 0);
+          mma_cols<D>(tmem + 256, tmem + 128, dKvM + slot(2 * t), t > 0);
           mma_commit(bar(L::kBarEmpty + (2 * t) % NS));
-          if (t == T - 1) mma_commit(bar(L::kBarFinal));
+          if (!more) mma_commit(bar(L::kBarFinal));
+        }
+        __syncwarp();
+      }
+      if (more) {
+        ok = full(v);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          mma_rows_ts<D>(tmem + 128, tmem + 448, dKv + slot(v));
+          mma_commit(bar(L::kBarDp));
+          mma_commit(bar(L::kBarEmpty + v % NS));
         }
         __syncwarp();
       }
@@ -281,17 +315,30 @@ __global__ void __launch_bounds__(kWThreads, 1)
     asm volatile("bar.sync 2, 256;" ::: "memory");
     const float nd = -dots[r];
     const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), nl = f2(nl2, nl2), nd2 = f2(nd, nd);
+    // Q and dO into TMEM, one by each group of warps.
     bool ok = true;
-    for (int t = 0; t < T; ++t) {
-      const uint32_t ts = tmem + (t & 1) * 128 + 64 * wg + lane_off;
+    if (T > 0) {
+      ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarIn), 0, kErrWbIn, abort_flag));
+      if (ok) {
+        row_to_tmem<D>(wg == 0 ? sQ : sDO, r, tmem + (wg == 0 ? 384 : 448) + lane_off);
+        tmem_st_wait();
+        tc_fence_before();
+        fence_async_smem();
+        mbar_arrive(bar(L::kBarTaken));
+      }
+    }
+    const uint32_t ts = tmem + 64 * wg + lane_off, tp = tmem + 128 + 64 * wg + lane_off;
+    for (int t = 0; ok && t < T; ++t) {
       const int key0 = kt.key0(t);
       const bool sink = t < kt.ns;
       const bool whole = sink ? key0 + kWTile <= min(kt.cut, all_hi) : key0 >= all_lo && key0 + kWTile <= all_hi;
-      ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarS + (t & 1)), (t >> 1) & 1, kErrWbS, abort_flag));
+      ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarS), t & 1, kErrWbS, abort_flag));
       if (!ok) break;
       tc_fence_after();
       float s[64], dp[64];
       tmem_ld64(ts, s);
+      tc_fence_before();
+      mbar_arrive(bar(L::kBarSFree));
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         const float2 x = f2_split(fma2(f2(s[2 * j], s[2 * j + 1]), sc2, nl));
@@ -311,16 +358,14 @@ __global__ void __launch_bounds__(kWThreads, 1)
       ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarDp), t & 1, kErrWbDp, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      tmem_ld64(tmem + 256 + 64 * wg + lane_off, dp);
-      tc_fence_before();
-      mbar_arrive(bar(L::kBarDpFree));
+      tmem_ld64(tp, dp);
       uint32_t pk[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         const float2 g = f2_split(add2(f2(dp[2 * j], dp[2 * j + 1]), nd2));
         pk[j] = pack_bf16x2(s[2 * j] * g.x, s[2 * j + 1] * g.y);
       }
-      tmem_st32(ts, pk);
+      tmem_st32(tp, pk);
       tc_fence_before();
       mbar_arrive(bar(L::kBarDs));
     }
@@ -330,7 +375,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     }
     // Each group of warps stores half of the channels.
     __nv_bfloat16* out = p.dQ + row * D + wg * (D / 2);
-    if (ok && T > 0) store_row<D / 2>(out, tmem + 384 + wg * (D / 2) + lane_off, p.scale, !live, i < p.N);
+    if (ok && T > 0) store_row<D / 2>(out, tmem + 256 + wg * (D / 2) + lane_off, p.scale, !live, i < p.N);
     else if (i < p.N) store_zero<D / 2>(out);
   } else {
     few_registers();
