@@ -362,18 +362,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
         if (live && p.lse) p.lse[row] = none ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
       } else {
         const int64_t slot = (int64_t)(2 * blockIdx.x + (start < unit0 ? 1 : 0)) * (2 * kWTile) + (x * tq * p.G + r);
-        float* out = p.part_o + slot * D;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32(to + c, o);
-          tmem_ld_wait();
-          if (live) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<float4*>(out + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-          }
-        }
+        store_row_f32<D>(p.part_o + slot * D, to, 1.0f, false, live);
         if (live) p.part_ml[slot] = make_float2(m_run, l_run);
       }
       tc_fence_before();

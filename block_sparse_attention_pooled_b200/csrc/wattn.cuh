@@ -115,21 +115,57 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&r)[32]) {
   for (int j = 0; j < 32; ++j) r[j] = __uint_as_float(v[j / 16][j % 16]);
 }
 
+// 32 bytes to global memory: in one piece where `wide` (the address is a
+// multiple of 32; a warp's rows then fill whole sectors), else in two.
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+__device__ __forceinline__ bool is_wide(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 // A row of D accumulator columns times f, as bf16.
 template <int D>
 __device__ __forceinline__ void store_row(__nv_bfloat16* out, uint32_t taddr, float f, bool zero, bool store) {
+  const bool wide = is_wide(out);
 #pragma unroll 1
   for (int c = 0; c < D; c += 32) {
     float o[32];
     tmem_ld32(taddr + c, o);
     tmem_ld_wait();
-    uint32_t w[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = zero ? 0u : pack_bf16x2(o[2 * j] * f, o[2 * j + 1] * f);
     if (store) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4*>(out + c + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = zero ? 0u : pack_bf16x2(o[16 * h + 2 * j] * f, o[16 * h + 2 * j + 1] * f);
+        store32(out + c + 16 * h, w, wide);
+      }
+    }
+  }
+}
+
+// The same in fp32 (out: a multiple of 32 bytes).
+template <int D>
+__device__ __forceinline__ void store_row_f32(float* out, uint32_t taddr, float f, bool zero, bool store) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    float o[32];
+    tmem_ld32(taddr + c, o);
+    tmem_ld_wait();
+    if (store) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = zero ? 0u : __float_as_uint(o[8 * h + j] * f);
+        store32(out + c + 8 * h, w, true);
+      }
     }
   }
 }
@@ -458,22 +494,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
         ++nq;
       }
       __nv_bfloat16* out = p.O + ((int64_t)bh * p.N + i) * D;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        float o[32];
-        if (kt.total > 0) {
-          tmem_ld32(to + c, o);
-          tmem_ld_wait();
-        }
-        uint32_t w[16];
+      if (kt.total > 0) {
+        store_row<D>(out, to, inv, !(l_run > 0.0f) && l_run == l_run, i < p.N);
+      } else if (i < p.N) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          w[j] = kt.total > 0 && l_run > 0.0f ? pack_bf16x2(o[2 * j] * inv, o[2 * j + 1] * inv) : 0u;
-        if (i < p.N) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(out + c + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        }
+        for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
       }
       if (kt.total > 0) {
         tc_fence_before();

@@ -671,17 +671,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
     if (pieces > 1) {
       const int64_t slot = part_slot(p, kvh, tile, piece);
       float* out = p.part + ((slot * 2 + wg) * kWTile + r) * D;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        float o[32];
-        if (ok && T > 0) {
-          tmem_ld32(acc + c, o);
-          tmem_ld_wait();
-        }
+      if (ok && T > 0) {
+        store_row_f32<D>(out, acc, f, !live, true);
+      } else {
 #pragma unroll
-        for (int k = 0; k < 32; k += 4)
-          *reinterpret_cast<float4*>(out + c + k) = ok && T > 0 && live ? make_float4(o[k] * f, o[k + 1] * f, o[k + 2] * f, o[k + 3] * f)
-                                                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int c = 0; c < D; c += 4) *reinterpret_cast<float4*>(out + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
     } else {
       __nv_bfloat16* out = (wg == 0 ? p.dV : p.dK) + ((int64_t)kvh * p.N + j) * D;
