@@ -374,6 +374,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     constexpr int CH = D / 16;             // 16-code pieces per row
     constexpr int N = kWTile * CH / 128;   // pieces per thread and tile
+    constexpr int U = 4;                   // at a time
     const int tid = threadIdx.x - 384, c = tid % CH, r0 = tid / CH;
     constexpr int RS = 128 / CH;           // rows between a thread's pieces
     uint32_t n = 0;
@@ -387,41 +388,44 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t there = code_mask[is_v], src = sbase + L::kOffCode + is_v * (kWTile * D);
-        uint4 code[N];
-        uint32_t power[N];  // 2^e as bf16, twice; 0 where the place does not exist
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const int r = r0 + k * RS;
-          const bool here = key0 + r < len && (there >> (r >> box_shift) & 1u);
-          const uint4 v = lds128(src + r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) * 16));
-          const uint32_t e = lds_u8(sbase + L::kOffExp + is_v * 128 + r);
-          code[k] = here ? v : make_uint4(0, 0, 0, 0);
-          power[k] = here ? (e == 255 ? 0x7FC0u : e << 7) * 0x10001u : 0u;
-        }
-        mbar_arrive(bar(L::kBarCodeEmpty + is_v));
         ok = n < NS || role_wait(bar(L::kBarKvEmpty + slot), (n / NS - 1) & 1, kErrCcKvEmpty, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t dst = sKv + slot * L::kTileBytes;
+        const uint32_t line0 = dst + (2 * c / 8) * (kWTile * 128);
+#pragma unroll 1
+        for (int k0 = 0; k0 < N; k0 += U) {
+          uint4 code[U];
+          uint32_t e[U];
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const int r = r0 + k * RS;
-          const uint32_t w[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
-          const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&power[k]);
-          uint32_t v[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t y = codes_to_bf16(__byte_perm(w[j / 2], 0, j & 1 ? 0x3424 : 0x1404));
-            const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), f);
-            v[j] = *reinterpret_cast<const uint32_t*>(&z);
+          for (int k = 0; k < U; ++k) {
+            const int r = r0 + (k0 + k) * RS;
+            code[k] = lds128(src + r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) * 16));
+            e[k] = lds_u8(sbase + L::kOffExp + is_v * 128 + r);
           }
-          const uint32_t line = dst + (2 * c / 8) * (kWTile * 128) + r * 128;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + ((((2 * c) % 8 + h) ^ (r & 7)) * 16)),
-                         "r"(v[4 * h]), "r"(v[4 * h + 1]), "r"(v[4 * h + 2]), "r"(v[4 * h + 3])
-                         : "memory");
+          for (int k = 0; k < U; ++k) {
+            const int r = r0 + (k0 + k) * RS;
+            const bool here = key0 + r < len && (there >> (r >> box_shift) & 1u);
+            const uint32_t power = here ? (e[k] == 255 ? 0x7FC0u : e[k] << 7) * 0x10001u : 0u;  // 2^e as bf16, twice
+            const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&power);
+            const uint32_t w[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
+            uint32_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t y = codes_to_bf16(__byte_perm(w[j / 2], 0, j & 1 ? 0x3424 : 0x1404));
+              const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), f);
+              v[j] = here ? *reinterpret_cast<const uint32_t*>(&z) : 0u;
+            }
+            const uint32_t line = line0 + r * 128;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(line + ((((2 * c) % 8 + h) ^ (r & 7)) * 16)),
+                           "r"(v[4 * h]), "r"(v[4 * h + 1]), "r"(v[4 * h + 2]), "r"(v[4 * h + 3])
+                           : "memory");
+          }
         }
+        mbar_arrive(bar(L::kBarCodeEmpty + is_v));
         fence_async_smem();
         mbar_arrive(bar(L::kBarKvFull + slot));
       }
