@@ -18,7 +18,8 @@
 // the other tile's softmax runs. Issue order per key tile:
 //   O_A += P_A(t) V(t); S_A(t+1) = Q_A K(t+1)^T; O_B += P_B(t) V(t); S_B(t+1).
 // The products complete in order, so "S(t+1) is there" also says that O(t) is,
-// and a row may be rescaled without a wait of its own.
+// and a row may be rescaled without a wait of its own. A key tile that none of
+// a row tile's rows see (the window's ends) is left out for that row tile.
 // TMEM columns: S_A [0,128), S_B [128,256), O_A [256,256+D), O_B [384,384+D);
 // P(t) (bf16, two per column) lies over the first 64 columns of its S(t).
 #pragma once
@@ -309,6 +310,18 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const int last = min(q0 + 2 * kWTile, len) - 1;
     kt = key_tiles(p.w.lo(q0), p.w.hi(last, len), p.w.sinks, 0);
   };
+  // Which of an item's key tiles the rows of its 128-row tile x see at all.
+  struct Reach {
+    int lo, hi, sinks;
+    __device__ __forceinline__ bool sees(int key0) const {
+      return key0 < hi && (key0 + kWTile > lo || key0 < sinks);
+    }
+  };
+  auto reach = [&](int x, int q0, int len) {
+    const int first = q0 + x * kWTile;
+    if (first >= len) return Reach{0, 0, 0};
+    return Reach{p.w.lo(first), p.w.hi(min(first + kWTile, len) - 1, len), p.w.sinks};
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -369,7 +382,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
     auto wait = [&](int b, uint32_t parity, unsigned int site) {
       return __all_sync(0xffffffffu, role_wait(bar(b), parity, site, abort_flag));
     };
-    uint32_t n = 0, nq = 0, np = 0;  // ring slots used, items, key tiles
+    uint32_t n = 0, nq = 0;                         // ring slots used, items
+    uint32_t steps0 = 0, steps1 = 0, done0 = 0, done1 = 0;  // key tiles and items of each row tile
     bool ok = true;
     auto issue_s = [&](int x, int slot) {  // S_x = Q_x K^T
       if (leader) {
@@ -388,57 +402,68 @@ __global__ void __launch_bounds__(kWThreads, 1)
       KeyTiles kt;
       item(it, bh, q0, len, kt);
       if (kt.total == 0) continue;
+      const Reach ra = reach(0, q0, len), rb = reach(1, q0, len);
+      bool begun0 = false, begun1 = false;
       ok = wait(L::kBarQFull, nq & 1, kErrWinQ) && wait(L::kBarKvFull + n % NS, (n / NS) & 1, kErrWinKvFull);
       if (!ok) break;
       tc_fence_after();
-      issue_s(0, n % NS);
-      issue_s(1, n % NS);
+      if (ra.sees(kt.key0(0))) issue_s(0, n % NS);
+      if (rb.sees(kt.key0(0))) issue_s(1, n % NS);
       if (leader) {
         mma_commit(bar(L::kBarKvEmpty + n % NS));
         if (kt.total == 1) mma_commit(bar(L::kBarQEmpty));
       }
       __syncwarp();
       ++n;
-      for (int t = 0; ok && t < kt.total; ++t, ++np) {
-        const int vs = n % NS, ks = (n + 1) % NS;
+      for (int t = 0; ok && t < kt.total; ++t) {
+        const int vs = n % NS, ks = (n + 1) % NS, key0 = kt.key0(t), key1 = kt.key0(t + 1);
         const bool more = t + 1 < kt.total;
+        ok = wait(L::kBarKvFull + vs, (n / NS) & 1, kErrWinKvFull);
+#pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (x == 0) ok = wait(L::kBarKvFull + vs, (n / NS) & 1, kErrWinKvFull);
-          if (ok && t == 0 && nq > 0) ok = wait(L::kBarOFree + x, (nq - 1) & 1, kErrWinOFree);
-          ok = ok && wait(L::kBarP + x, np & 1, kErrWinP);
-          if (!ok) break;
-          tc_fence_after();
-          if (leader) {
+          const Reach& r = x == 0 ? ra : rb;
+          uint32_t &steps = x == 0 ? steps0 : steps1, &done = x == 0 ? done0 : done1;
+          bool& begun = x == 0 ? begun0 : begun1;
+          if (ok && r.sees(key0)) {
+            if (!begun && done > 0) ok = wait(L::kBarOFree + x, (done - 1) & 1, kErrWinOFree);
+            ok = ok && wait(L::kBarP + x, steps & 1, kErrWinP);
+            if (!ok) break;
+            tc_fence_after();
             const uint64_t v = dVm + (uint64_t)((vs * L::kTileBytes) >> 4);
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < kWTile / 32; ++kk)  // 16 keys = 2048 bytes of V = 8 columns of P
-              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, v + kk * 128, idO, (t > 0 || kk > 0) ? 1u : 0u);
-          }
-          __syncwarp();
-          ok = wait(L::kBarP2 + x, np & 1, kErrWinP);
-          if (!ok) break;
-          tc_fence_after();
-          if (leader) {
-            const uint64_t v = dVm + (uint64_t)((vs * L::kTileBytes) >> 4);
+              for (int kk = 0; kk < kWTile / 32; ++kk)  // 16 keys = 2048 bytes of V = 8 columns of P
+                mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, v + kk * 128, idO, (begun || kk > 0) ? 1u : 0u);
+            }
+            __syncwarp();
+            ok = wait(L::kBarP2 + x, steps & 1, kErrWinP);
+            if (!ok) break;
+            tc_fence_after();
+            const bool last = t == kt.ns + (r.hi - 1 - kt.lo) / kWTile;  // holds the last key it sees
+            if (leader) {
 #pragma unroll
-            for (int kk = kWTile / 32; kk < kWTile / 16; ++kk)
-              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, v + kk * 128, idO, 1u);
-            if (x == 1) mma_commit(bar(L::kBarKvEmpty + vs));
-            if (!more) mma_commit(bar(L::kBarO + x));
+              for (int kk = kWTile / 32; kk < kWTile / 16; ++kk)
+                mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, v + kk * 128, idO, 1u);
+              if (last) mma_commit(bar(L::kBarO + x));
+            }
+            __syncwarp();
+            begun = true;
+            ++steps;
+            if (last) ++done;
           }
-          __syncwarp();
-          if (more) {
-            if (x == 0) ok = wait(L::kBarKvFull + ks, ((n + 1) / NS) & 1, kErrWinKvFull);
+          if (ok && more && r.sees(key1)) {
+            ok = wait(L::kBarKvFull + ks, ((n + 1) / NS) & 1, kErrWinKvFull);
             if (!ok) break;
             tc_fence_after();
             issue_s(x, ks);
-            if (x == 1 && leader) {
-              mma_commit(bar(L::kBarKvEmpty + ks));
-              if (t + 2 == kt.total) mma_commit(bar(L::kBarQEmpty));
-            }
-            __syncwarp();
           }
         }
+        if (ok && leader) {
+          mma_commit(bar(L::kBarKvEmpty + vs));
+          if (more) mma_commit(bar(L::kBarKvEmpty + ks));
+          if (t + 2 == kt.total) mma_commit(bar(L::kBarQEmpty));
+        }
+        __syncwarp();
         n += more ? 2 : 1;
       }
       ++nq;
@@ -467,40 +492,44 @@ __global__ void __launch_bounds__(kWThreads, 1)
       const int lo = p.w.lo(at), hi = p.w.hi(at, len);
       // Keys that all rows of the warp see without looking at the sinks.
       const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
+      const Reach rx = reach(x, q0, len);
       float m_run = -INFINITY, l_run = 0.0f;
-      for (int t = 0; t < kt.total; ++t, ++np) {
+      bool begun = false;
+      for (int t = 0; t < kt.total; ++t) {
         const int key0 = kt.key0(t);
-        ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarS + x), np & 1, kErrWinS, abort_flag));
+        if (!rx.sees(key0)) continue;
+        ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarS + x), np++ & 1, kErrWinS, abort_flag));
         if (!ok) break;
         tc_fence_after();
         const bool sink = t < kt.ns;
         const bool whole = sink ? key0 + kWTile <= min(kt.cut, all_hi) : key0 >= all_lo && key0 + kWTile <= all_hi;
         const int e = (sink ? min(hi, kt.cut) : hi) - key0;
-        softmax_tile<D>(ts, to, t == 0, whole, sink ? 0 : lo - key0, e, p.w.sinks - key0, p.scale_log2, m_run, l_run,
+        softmax_tile<D>(ts, to, !begun, whole, sink ? 0 : lo - key0, e, p.w.sinks - key0, p.scale_log2, m_run, l_run,
                         0, [&] {
                           tc_fence_before();
                           mbar_arrive(bar(L::kBarP + x));
                         });
         tc_fence_before();
         mbar_arrive(bar(L::kBarP2 + x));
+        begun = true;
       }
       if (!ok) break;
       if (i >= len) l_run = 0.0f;
       const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
-      if (kt.total > 0) {
+      if (begun) {
         ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarO + x), nq & 1, kErrWinO, abort_flag));
         if (!ok) break;
         tc_fence_after();
         ++nq;
       }
       __nv_bfloat16* out = p.O + ((int64_t)bh * p.N + i) * D;
-      if (kt.total > 0) {
+      if (begun) {
         store_row<D>(out, to, inv, !(l_run > 0.0f) && l_run == l_run, i < p.N);
       } else if (i < p.N) {
 #pragma unroll
         for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
       }
-      if (kt.total > 0) {
+      if (begun) {
         tc_fence_before();
         mbar_arrive(bar(L::kBarOFree + x));
       }

@@ -37,8 +37,8 @@ bool all_aligned16(std::initializer_list<const void*> ps) {
 // A key that every later row sees (a sink, or any key where the past is not
 // limited) has up to N rows per head, another as many as the window is wide;
 // one CTA works through its rows in order, so long runs are cut into pieces of
-// at most about a third of an SM's share of the whole work (but of 8 tiles at
-// least: a piece's fp32 sums are written and read once more).
+// at most about a third of an SM's share of the whole work, or about its share
+// where that is small (a piece's fp32 sums are written and read once more).
 struct KvSplit {
   int tiles, sink_tiles, sink_pieces, pieces;
   size_t slots;  // of [2][128][d] fp32
@@ -53,9 +53,17 @@ KvSplit kv_split(const sparge_window_shape* s, const sparge_window* w, const WDi
   k.sink_tiles = w->left < 0 ? 0 : (int)ceil_div(std::min(w->sinks, s->N), kWTile);
   const int64_t run = G * ceil_div(reach, kWTile), sink_run = G * k.tiles;
   const int64_t all = d.BHkv * (run * (k.tiles - k.sink_tiles) + sink_run * k.sink_tiles);
-  const int64_t most = std::max<int64_t>(8, all / (3 * 148));
-  k.pieces = (int)std::min<int64_t>(ceil_div(run, most), 64);
-  k.sink_pieces = (int)std::min<int64_t>(ceil_div(sink_run, most), 64);
+  // Little work is dealt in one piece per SM (a second round of CTAs would take
+  // as long as the first).
+  const int64_t sms = 148, share = ceil_div(all, sms);
+  int64_t most = share > 24 ? share / 3 : std::max<int64_t>(8, share);
+  for (;; ++most) {
+    k.pieces = (int)std::min<int64_t>(ceil_div(run, most), 64);
+    k.sink_pieces = (int)std::min<int64_t>(ceil_div(sink_run, most), 64);
+    if (share > 24 || most >= sink_run ||
+        d.BHkv * ((int64_t)k.sink_tiles * k.sink_pieces + (int64_t)(k.tiles - k.sink_tiles) * k.pieces) <= sms)
+      break;
+  }
   k.slots = k.sink_pieces > 1 ? (size_t)d.BHkv * k.sink_tiles * k.sink_pieces : 0;
   if (k.pieces > 1) k.slots += (size_t)d.BHkv * (k.tiles - k.sink_tiles) * k.pieces;
   return k;
