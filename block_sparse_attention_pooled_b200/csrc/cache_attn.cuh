@@ -513,7 +513,8 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
     const bool all = at0 == 0 && stop == it.T;
     if (at0 == 0 && threadIdx.x < tokens)
       p.owners[(int64_t)(it.cu + t0 + threadIdx.x) * p.c.Hkv + it.hk] =
-          make_int2(blockIdx.x | (start < unit0 ? 1 << 30 : 0), all ? (int)blockIdx.x : run_owner(W, ctas, unit0 + it.T - 1));
+          make_int4(blockIdx.x, start < unit0, all ? (int)blockIdx.x : run_owner(W, ctas, unit0 + it.T - 1),
+                    threadIdx.x * p.G);
     const int64_t slot0 = (int64_t)(2 * blockIdx.x + (start < unit0 ? 1 : 0)) * L::kRows;
     constexpr int TPR = D / 4;  // threads per row, four channels each
     for (int r = threadIdx.x / TPR; r < tokens * p.G; r += NW * 32 / TPR) {  // NW * 32 is a multiple of TPR

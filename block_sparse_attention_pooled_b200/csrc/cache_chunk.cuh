@@ -355,8 +355,8 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
       const bool none = l_run == 0.0f;
       if (at0 == 0 && live && r % p.G == 0)
         p.owners[(int64_t)(it.cu + tok) * p.c.Hkv + it.hk] =
-            make_int2(blockIdx.x | (start < unit0 ? 1 << 30 : 0),
-                      stop == it.T ? (int)blockIdx.x : run_owner(W, ctas, unit0 + it.T - 1));
+            make_int4(blockIdx.x, start < unit0, stop == it.T ? (int)blockIdx.x : run_owner(W, ctas, unit0 + it.T - 1),
+                      x * tq * p.G + r);
       if (at0 == 0 && stop == it.T) {
         store_row<D>(p.O + row * D, to, none ? 0.0f : 1.0f / l_run, none, live);
         if (live && p.lse) p.lse[row] = none ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;

@@ -49,7 +49,7 @@ struct CacheAttnParams {
   float* lse;
   float* part_o;    // [2 * CTAs][rows][D]: a CTA's first and last partial
   float2* part_ml;  // [2 * CTAs][rows]: reference (log2) and sum
-  int2* owners;     // [tokens][Hkv]: first CTA of the token's item (bit 30: its last partial) and last CTA
+  int4* owners;     // [tokens][Hkv]: first CTA of the token's item, whether in its last partial, last CTA, row of head 0
   int H, G;
   int tpt;          // tokens per row tile
   int box_shift;    // log2 of the keys in one TMA box of pages
@@ -240,20 +240,18 @@ __device__ __forceinline__ int run_owner(int64_t W, int ctas, int64_t u) {
 }
 
 // One warp per (packed token, head): joins the partials of the item that the
-// token's rows lie in, if there is more than one. ROWS: rows of a partial.
+// token's rows lie in, if there is more than one. rows: of a partial.
 template <int D>
 __global__ void __launch_bounds__(128) cache_combine_kernel(const CacheAttnParams p, int rows) {
-  constexpr int C = D / 32;
+  constexpr int C = D / 32;  // neighbouring channels per lane
   const int lane = threadIdx.x % 32;
   const int64_t id = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-  const int t = (int)(id / p.H), h = (int)(id % p.H), hk = h / p.G;
+  const int t = (int)(id / p.H), h = (int)(id % p.H);
   if (t >= min(__ldg(p.c.cu + p.c.B), p.c.tokens)) return;
-  const int2 own = p.owners[(int64_t)t * p.c.Hkv + hk];
-  const int c0 = own.x & 0x3FFFFFFF, c1 = own.y;
+  const int4 own = p.owners[(int64_t)t * p.c.Hkv + h / p.G];
+  const int c0 = own.x, c1 = own.z, r = own.w + h % p.G;
   if (c0 == c1) return;  // one CTA did it all
-  const int place = t - __ldg(p.c.cu + find_seq(p.c.cu, p.c.B, t));
-  const int r = place % p.tpt * p.G + h % p.G;
-  auto slot = [&](int c) { return (int64_t)(2 * c + (c == c0 ? own.x >> 30 : 0)) * rows + r; };
+  auto slot = [&](int c) { return (int64_t)(2 * c + (c == c0 ? own.y : 0)) * rows + r; };
   float m = -INFINITY;
   for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[slot(c)].x);
 #pragma unroll
@@ -267,15 +265,23 @@ __global__ void __launch_bounds__(128) cache_combine_kernel(const CacheAttnParam
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const float fi = __shfl_sync(0xffffffffu, f, i);
-      const float* src = p.part_o + slot(b + i) * D + lane;
+      const float* src = p.part_o + slot(b + i) * D + lane * C;
+      float v[C];
+      if (C == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
 #pragma unroll
-      for (int k = 0; k < C; ++k) o[k] += src[k * 32] * fi;
+      for (int k = 0; k < C; ++k) o[k] += v[k] * fi;
     }
   }
   l = warp_sum(l);
   const int64_t row = (int64_t)t * p.H + h;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint32_t w[C / 2];
 #pragma unroll
-  for (int k = 0; k < C; ++k) p.O[row * D + k * 32 + lane] = __float2bfloat16_rn(l == 0.0f ? 0.0f : o[k] / l);
+  for (int k = 0; k < C / 2; ++k) w[k] = pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
+  __nv_bfloat16* out = p.O + row * D + lane * C;
+  if (C == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[C / 2 - 1]);
+  else *reinterpret_cast<uint32_t*>(out) = w[0];
   if (p.lse && lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 

@@ -515,7 +515,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       if (!ok) break;
       if (i >= len) l_run = 0.0f;
-      const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
+      const bool none = l_run == 0.0f;
+      const float inv = none ? 0.0f : 1.0f / l_run;
       if (begun) {
         ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarO + x), nq & 1, kErrWinO, abort_flag));
         if (!ok) break;
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       __nv_bfloat16* out = p.O + ((int64_t)bh * p.N + i) * D;
       if (begun) {
-        store_row<D>(out, to, inv, !(l_run > 0.0f) && l_run == l_run, i < p.N);
+        store_row<D>(out, to, inv, none, i < p.N);
       } else if (i < p.N) {
 #pragma unroll
         for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         mbar_arrive(bar(L::kBarOFree + x));
       }
       if (p.lse != nullptr && i < p.N)
-        p.lse[(int64_t)bh * p.N + i] = l_run > 0.0f ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+        p.lse[(int64_t)bh * p.N + i] = l_run == 0.0f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
     }
   } else {
     few_registers();

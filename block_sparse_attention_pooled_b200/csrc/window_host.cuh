@@ -215,7 +215,7 @@ AttnPlan attn_plan(const sparge_cache* c, const sparge_cache_batch* b, int32_t H
   a.tpt = a.rows <= 16 ? (int)(a.rows / G) : (int)(kWTile / G) * 2;
   a.ctas = sm_count();
   a.owners = align256((size_t)2 * a.ctas * a.rows * 8) + align256((size_t)2 * a.ctas * a.rows * c->d * 4);
-  a.bytes = a.owners + align256((size_t)b->tokens * c->Hkv * 8);
+  a.bytes = a.owners + align256((size_t)b->tokens * c->Hkv * 16);
   return a;
 }
 
@@ -395,7 +395,7 @@ sparge_status sparge_cache_attn(const sparge_cache* cache, const sparge_cache_ba
   p.lse = lse;
   p.part_ml = static_cast<float2*>(workspace);
   p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + align256((size_t)2 * plan.ctas * plan.rows * 8));
-  p.owners = reinterpret_cast<int2*>(static_cast<uint8_t*>(workspace) + plan.owners);
+  p.owners = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + plan.owners);
   p.H = H;
   p.G = H / cache->Hkv;
   p.tpt = plan.tpt;

@@ -343,3 +343,32 @@ def test_a_large_batch_again_and_again(sparge, kind, H):
         for h in range(0, H, 3):
             o, _, to, _, _ = rows_fwd(Q[b:b + 1, h], ks[b][h // (H // Hkv)], vs[b][h // (H // Hkv)], seen)
             close(runs[0][b:b + 1, h], o, to, f"sequence {b}, head {h}")
+
+
+@pytest.mark.parametrize("new", [1, 50])
+def test_a_row_of_the_cache_that_is_nan(sparge, new):
+    """A token written with an infinity reads as NaN and makes the rows that see it NaN; rows that do not see it, and a
+    row whose window has passed it, stay as they are."""
+    c = Paged("e4m3", 1, 128, 32, [200 + new])
+    k, v = c.normal(200 + new, 1, 128), c.normal(200 + new, 1, 128)
+    k[150, 0, 3] = math.inf
+    cu, first = ints(0, 200 + new), ints(0)
+    sparge.sparge_cache_write(k, v, c.k, c.v, c.table, first, cu, **c.exp)
+    K, V = sparge.sparge_cache_read(c.k, c.v, c.table, first, cu, 200 + new, **c.exp)
+    assert torch.isnan(K[150]).all() and torch.isfinite(V).all() and torch.isfinite(K[151:]).all()
+    Q = c.normal(new, 4, 128)
+    for left, seen in ((-1, True), (20, False)):
+        lse = torch.empty(new, 4, device="cuda")
+        O = sparge.sparge_cache_attn(Q, c.k, c.v, c.table, ints(200), ints(0, new), new, 200 + new, left, 0, lse=lse, **c.exp)
+        assert torch.isnan(O).all() == seen and torch.isnan(lse).all() == seen and torch.isfinite(O).all() == (not seen)
+
+
+@pytest.mark.parametrize("new", [1, 60])
+def test_output_at_any_16_bytes(sparge, new):
+    c = Paged("bf16", 2, 64, 16, [300])
+    c.fill(sparge, [300])
+    Q = c.normal(new, 4, 64)
+    args = (Q, c.k, c.v, c.table, ints(300 - new), ints(0, new), new, 300)
+    want = sparge.sparge_cache_attn(*args)
+    odd = torch.empty(Q.numel() + 8, dtype=torch.bfloat16, device="cuda")[8:].view(Q.shape)
+    assert odd.data_ptr() % 32 == 16 and torch.equal(sparge.sparge_cache_attn(*args, O=odd), want)

@@ -201,3 +201,28 @@ def test_given_outputs_are_used(sparge):
     out = [torch.empty_like(t) for t in (Q, K, V)]
     got = sparge.sparge_window_bwd(Q, K, V, O, lse, dO, 10, 0, dQ=out[0], dK=out[1], dV=out[2])
     assert all(a is b for a, b in zip(got, out))
+
+
+def test_outputs_at_any_16_bytes(sparge):
+    """Outputs whose address is a multiple of 16 but not of 32 bytes."""
+    Q, K, V, dO = inputs(1, 2, 1, 150, 128, seed=10)
+    lse = torch.empty(1, 2, 150, device="cuda")
+    O = sparge.sparge_window_fwd(Q, K, V, 30, 0, lse=lse)
+    G = sparge.sparge_window_bwd(Q, K, V, O, lse, dO, 30, 0)
+    odd = [torch.empty(t.numel() + 8, dtype=torch.bfloat16, device="cuda")[8:].view(t.shape) for t in (Q, Q, K, V)]
+    sparge.sparge_window_fwd(Q, K, V, 30, 0, O=odd[0])
+    sparge.sparge_window_bwd(Q, K, V, O, lse, dO, 30, 0, dQ=odd[1], dK=odd[2], dV=odd[3])
+    for a, b in zip(odd, (O,) + G):
+        assert a.data_ptr() % 32 == 16 and torch.equal(a, b)
+
+
+def test_a_row_of_nan_stays_a_row(sparge):
+    """A NaN in one query row gives that row NaN, in O and the log-sum-exp, and no other."""
+    Q, K, V, _ = inputs(1, 1, 1, 300, 64, seed=12)
+    lse, clean = torch.empty(1, 1, 300, device="cuda"), torch.empty(1, 1, 300, device="cuda")
+    want = sparge.sparge_window_fwd(Q, K, V, -1, 0, lse=clean)
+    Q[0, 0, 77, 5] = float("nan")
+    O = sparge.sparge_window_fwd(Q, K, V, -1, 0, lse=lse)
+    assert torch.isnan(O[0, 0, 77]).all() and torch.isnan(lse[0, 0, 77])
+    keep = torch.arange(300, device="cuda") != 77
+    assert torch.equal(O[0, 0, keep], want[0, 0, keep]) and torch.equal(lse[0, 0, keep], clean[0, 0, keep])
