@@ -36,7 +36,7 @@ namespace sparge {
 
 enum : unsigned int {
   kErrWinQ = 0x900, kErrWinQEmpty, kErrWinKvFull, kErrWinKvEmpty, kErrWinS, kErrWinP, kErrWinO, kErrWinOFree,
-  kErrWinDrain, kErrWinFix
+  kErrWinDrain, kErrWinFix, kErrWinNext
 };
 
 constexpr int kWTile = 128;       // rows per tile and keys per tile
@@ -47,7 +47,7 @@ struct WAttnParams {
   const int32_t* lens;  // whole sequences: [B] or null
   __nv_bfloat16* O;
   float* lse;
-  int B, H, Hkv, N, items, rtiles;
+  int B, H, Hkv, N, rtiles;
   float scale_log2;
 };
 
@@ -60,9 +60,10 @@ struct WSmem {
   static constexpr int kOffBar = kOffKv + NS * kTileBytes;
   static constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarKvFull = 2, kBarKvEmpty = 2 + NS, kBarS = 2 + 2 * NS,
                        kBarP = 4 + 2 * NS, kBarP2 = 6 + 2 * NS, kBarO = 8 + 2 * NS, kBarOFree = 10 + 2 * NS,
-                       kBarDrain = 12 + 2 * NS, kBarFix = 13 + 2 * NS;
-  static constexpr int kNumBars = 14 + 2 * NS;
-  static constexpr int kOffTmem = kOffBar + kNumBars * 8;
+                       kBarDrain = 12 + 2 * NS, kBarFix = 13 + 2 * NS, kBarNext = 14 + 2 * NS, kBarNextRead = 16 + 2 * NS;
+  static constexpr int kNumBars = 18 + 2 * NS;
+  static constexpr int kOffNext = kOffBar + kNumBars * 8;  // two answers of 16 bytes
+  static constexpr int kOffTmem = kOffNext + 32;
   static constexpr int kBytes = kOffTmem + 16 + 1024;
 };
 
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
       const bool rows = (i >= L::kBarP && i < L::kBarP + 4) || (i >= L::kBarOFree && i < L::kBarOFree + 2);
-      mbar_init(bar(i), rows ? 128 : 1);
+      mbar_init(bar(i), rows ? 128 : i >= L::kBarNextRead && i < L::kBarNextRead + 2 ? 10 : 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -295,6 +296,26 @@ __global__ void __launch_bounds__(kWThreads, 1)
   // The block's registers (384 x 168) are shared out anew: the first four
   // warps keep 80 each, so that the softmax's eight can hold a row's 128 scores.
   auto few_registers = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); };
+
+  // The block starts with the item of its index and then takes over items of
+  // blocks that have not started: each SM gets its next item when it is free
+  // (dealing them out in turn left 7% of the SMs' time unused on the 480p clip,
+  // a quarter on a ragged batch of three). Answers go through two slots that
+  // the ten warps with a role read.
+  struct Items {
+    uint32_t k;  // answers read
+  };
+  auto next_item = [&](Items& items) {
+    const int slot = items.k & 1;
+    const bool ok = role_wait(bar(L::kBarNext + slot), (items.k >> 1) & 1, kErrWinNext, abort_flag);
+    if (!__all_sync(0xffffffffu, ok)) return -1;
+    const int id = canceled_block(sbase + L::kOffNext + 16 * slot);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(L::kBarNextRead + slot));
+    ++items.k;
+    return id;
+  };
 
   // Work item `it`: rows [q0, q0 + 256) of head bh. The last rows come first:
   // they see the most where the past is not limited.
@@ -328,8 +349,22 @@ __global__ void __launch_bounds__(kWThreads, 1)
     few_registers();
     uint32_t n = 0, nq = 0;  // ring slots filled, items with work
     FixUp fix{bar(L::kBarFix), 0};
+    Items items{0};
     bool ok = true;
-    for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+    // Asked for when the item's loads are all on their way (earlier, and a long
+    // item would hold another back); the ring covers the answer's time.
+    auto ask = [&] {
+      const int slot = items.k & 1;
+      const bool free = items.k < 2 || role_wait(bar(L::kBarNextRead + slot), ((items.k >> 1) - 1) & 1, kErrWinNext, abort_flag);
+      if (!__all_sync(0xffffffffu, free)) return -1;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(L::kBarNext + slot), 16);
+        try_cancel(sbase + L::kOffNext + 16 * slot, bar(L::kBarNext + slot));
+      }
+      __syncwarp();
+      return next_item(items);
+    };
+    for (int it = blockIdx.x; ok && it >= 0; it = ok ? ask() : -1) {
       int bh, q0, len;
       KeyTiles kt;
       item(it, bh, q0, len, kt);
@@ -397,7 +432,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       __syncwarp();
     };
-    for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+    Items items{0};
+    for (int it = blockIdx.x; ok && it >= 0; it = ok ? next_item(items) : -1) {
       int bh, q0, len;
       KeyTiles kt;
       item(it, bh, q0, len, kt);
@@ -481,7 +517,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const uint32_t ts = tmem + x * 128 + lane_off, to = tmem + 256 + x * 128 + lane_off;
     uint32_t nq = 0, np = 0;
     bool ok = true;
-    for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+    Items items{0};
+    for (int it = blockIdx.x; ok && it >= 0; it = ok ? next_item(items) : -1) {
       int bh, q0, len;
       KeyTiles kt;
       item(it, bh, q0, len, kt);

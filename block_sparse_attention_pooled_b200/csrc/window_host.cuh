@@ -112,11 +112,10 @@ sparge_status launch_window_fwd(const void* Q, const void* K, const void* V, con
   p.N = s->N;
   p.rtiles = (int)ceil_div(s->N, 2 * kWTile);
   if (dm.BH * p.rtiles > INT32_MAX / 2) return SPARGE_ERR_UNSUPPORTED;
-  p.items = (int)(dm.BH * p.rtiles);
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
   cudaError_t e = ensure_smem(window_fwd_kernel<D>, WSmem<D>::kBytes, D == 64 ? 20 : 21);
   if (e != cudaSuccess) return cuda_status(e);
-  window_fwd_kernel<D><<<std::min(p.items, sm_count()), kWThreads, WSmem<D>::kBytes,
+  window_fwd_kernel<D><<<(unsigned)(dm.BH * p.rtiles), kWThreads, WSmem<D>::kBytes,
                          static_cast<cudaStream_t>(stream)>>>(mq, mk, mv, p);
   return cuda_status(cudaGetLastError());
 }
