@@ -373,15 +373,15 @@ def _want(t, name, dtype, shape, device):
 
 
 def _window_args(Q, K, V, left, right, sinks, unit, lens):
-    if Q.dtype != _BF16 or not Q.is_cuda or Q.dim() != 4 or not Q.is_contiguous() or K.dim() != 4:
+    qs, ks, device = Q.shape, K.shape, Q.device
+    index = device.index
+    if (Q.dtype is not _BF16 or K.dtype is not _BF16 or V.dtype is not _BF16 or not Q.is_cuda or len(qs) != 4
+            or len(ks) != 4 or ks != V.shape or ks[0] != qs[0] or ks[2:] != qs[2:] or K.get_device() != index
+            or V.get_device() != index or not Q.is_contiguous() or not K.is_contiguous() or not V.is_contiguous()):
         raise ValueError("Q, K, V must be contiguous bf16 CUDA tensors of shape [B,H,N,d] and [B,Hkv,N,d]")
-    B, H, N, d = Q.shape
-    Hkv = K.shape[1]
-    kv, device = (B, Hkv, N, d), Q.device
-    _want(K, "K", _BF16, kv, device)
-    _want(V, "V", _BF16, kv, device)
+    B, H, N, d = qs
     plens = None if lens is None else _want(lens, "lens", _I32, (B,), device)
-    return _pack_wshape(B, H, Hkv, N, d), _pack_window(left, right, sinks, unit), plens, kv, device
+    return _pack_wshape(B, H, ks[1], N, d), _pack_window(left, right, sinks, unit), plens, device
 
 
 def sparge_window_fwd(Q, K, V, left: int, right: int, sinks: int = 0, unit: int = 1, lens=None, O=None, lse=None,
@@ -389,7 +389,7 @@ def sparge_window_fwd(Q, K, V, left: int, right: int, sinks: int = 0, unit: int 
     """Attention with a sliding window and sinks over [B,H,N,d] (K, V: [B,Hkv,N,d]); left and right count units of
     `unit` tokens, -1 for no limit; lens: int32 [B] lengths of a padded batch. Returns O (and fills lse if given).
     It needs no workspace."""
-    shape, window, plens, _, device = _window_args(Q, K, V, left, right, sinks, unit, lens)
+    shape, window, plens, device = _window_args(Q, K, V, left, right, sinks, unit, lens)
     made = ()
     if O is None:
         O = torch.empty_like(Q)
@@ -402,15 +402,15 @@ def sparge_window_fwd(Q, K, V, left: int, right: int, sinks: int = 0, unit: int 
     return O
 
 
-def _space(workspace, n, device, made):
-    """Address and bytes of the workspace: the caller's, or n bytes taken here and added to `made`."""
+def _space(workspace, n, like, made):
+    """Address and bytes of the workspace: the caller's, or n bytes taken here, as `like`'s type, and added to `made`."""
     if workspace is None:
         if n == 0:
             return None, 0
-        workspace = torch.empty(n, dtype=_U8, device=device)
+        workspace = like.new_empty(-(-n // like.element_size()))
         made.append(workspace)
         return workspace.data_ptr(), n
-    if workspace.device != device or not workspace.is_contiguous():
+    if workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the inputs' device")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
@@ -418,7 +418,7 @@ def _space(workspace, n, device, made):
 def sparge_window_bwd(Q, K, V, O, lse, dO, left: int, right: int, sinks: int = 0, unit: int = 1, lens=None, dQ=None,
                       dK=None, dV=None, workspace=None, stream=None):
     """Gradients of sparge_window_fwd (O and lse from that call) for dL/dO = dO. Returns (dQ, dK, dV)."""
-    shape, window, plens, kv, device = _window_args(Q, K, V, left, right, sinks, unit, lens)
+    shape, window, plens, device = _window_args(Q, K, V, left, right, sinks, unit, lens)
     pO, pdO = _want(O, "O", _BF16, Q.shape, device), _want(dO, "dO", _BF16, Q.shape, device)
     plse = _want(lse, "lse", _F32, Q.shape[:3], device)
     made = []
@@ -431,7 +431,7 @@ def sparge_window_bwd(Q, K, V, O, lse, dO, left: int, right: int, sinks: int = 0
             _want(t, name, _BF16, like.shape, device)
         out.append(t)
     n = _lib.sparge_window_workspace_bytes(OP_WINDOW_BWD, shape, window) if workspace is None else 0
-    ws, nws = _space(workspace, n, device, made)
+    ws, nws = _space(workspace, n, lse, made)
     _launch(_lib.sparge_window_bwd, (Q.data_ptr(), K.data_ptr(), V.data_ptr(), shape, window, plens, pO, plse, pdO,
                                      out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws, nws), device, stream,
             made)
@@ -439,45 +439,51 @@ def sparge_window_bwd(Q, K, V, O, lse, dO, left: int, right: int, sinks: int = 0
 
 
 def _cache_args(k_pages, v_pages, k_exp, v_exp, page_table, first, cu, tokens):
-    """The two C structs of a paged cache and a batch of its sequences."""
-    if not k_pages.is_cuda or k_pages.dim() != 4:
-        raise ValueError("the cache's pages must be CUDA tensors of shape [pages, Hkv, page, d]")
+    """The two C structs of a paged cache and a batch of its sequences, and the device."""
     device, dtype, shape = k_pages.device, k_pages.dtype, k_pages.shape
-    pk, pv = _want(k_pages, "k_pages", dtype, shape, device), _want(v_pages, "v_pages", dtype, shape, device)
-    if dtype == _BF16:
+    index = device.index
+    if (not k_pages.is_cuda or len(shape) != 4 or v_pages.dtype is not dtype or v_pages.shape != shape
+            or v_pages.get_device() != index or not k_pages.is_contiguous() or not v_pages.is_contiguous()):
+        raise ValueError("the cache's pages must be contiguous CUDA tensors of one type and of shape [pages, Hkv, page, d]")
+    if dtype is _BF16:
         kind, ek, ev = CACHE_BF16, 0, 0
         if k_exp is not None or v_exp is not None:
             raise ValueError("a bf16 cache has no exponents")
-    elif dtype == _E4M3:
+    elif dtype is _E4M3:
         if k_exp is None or v_exp is None:
             raise ValueError("an e4m3 cache needs k_exp and v_exp")
         kind = CACHE_E4M3
         ek, ev = _want(k_exp, "k_exp", _U8, shape[:3], device), _want(v_exp, "v_exp", _U8, shape[:3], device)
     else:
         raise ValueError("a cache holds bfloat16 or float8_e4m3fn")
-    if page_table.dim() != 2 or page_table.dtype != _I32:
-        raise ValueError("page_table must be an int32 tensor of shape [B, max_pages]")
-    B, most = page_table.shape
-    pt = _want(page_table, "page_table", _I32, (B, most), device)
-    pf, pc = _want(first, "first", _I32, (B,), device), _want(cu, "cu", _I32, (B + 1,), device)
-    return _pack_cache(pk, pv, ek, ev, *shape, kind), _pack_batch(pt, pf, pc, B, most, tokens), device
+    table = page_table.shape
+    B = table[0] if len(table) == 2 else -1
+    if (B < 0 or page_table.dtype is not _I32 or first.dtype is not _I32 or cu.dtype is not _I32 or first.shape != (B,)
+            or cu.shape != (B + 1,) or page_table.get_device() != index or first.get_device() != index
+            or cu.get_device() != index or not page_table.is_contiguous() or not first.is_contiguous()
+            or not cu.is_contiguous()):
+        raise ValueError(f"page_table [B, max_pages], first [B] and cu [B + 1] must be contiguous int32 tensors on {device}")
+    return (_pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), ek, ev, *shape, kind),
+            _pack_batch(page_table.data_ptr(), first.data_ptr(), cu.data_ptr(), B, table[1], tokens), device)
 
 
 def _token_rows(t, name, heads, d, device):
     """Address and token stride of packed tokens [T, heads, d]: heads and channels contiguous, tokens any stride."""
-    if t.dtype is not _BF16 or t.get_device() != device.index or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or (
-            t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d))):
+    shape, stride = t.shape, t.stride()
+    if (t.dtype is not _BF16 or t.get_device() != device.index or len(shape) != 3 or shape[1] != heads or shape[2] != d
+            or (shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != d)))):
         raise ValueError(f"{name} must be a bf16 tensor of shape [tokens, {heads}, {d}] on {device}, contiguous within a token")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * d
+    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * d
 
 
 def sparge_cache_write(k, v, k_pages, v_pages, page_table, first, cu_new, k_exp=None, v_exp=None, stream=None) -> None:
     """Writes new tokens' k, v (bf16 [T,Hkv,d], any token stride) into the paged cache at positions first[b], ..."""
-    cache, batch, device = _cache_args(k_pages, v_pages, k_exp, v_exp, page_table, first, cu_new, k.shape[0])
+    T = k.shape[0]
+    cache, batch, device = _cache_args(k_pages, v_pages, k_exp, v_exp, page_table, first, cu_new, T)
     _, Hkv, _, d = k_pages.shape
     pk, sk = _token_rows(k, "k", Hkv, d, device)
     pv, sv = _token_rows(v, "v", Hkv, d, device)
-    if v.shape[0] != k.shape[0]:
+    if v.shape[0] != T:
         raise ValueError("k and v must hold the same tokens")
     _launch(_lib.sparge_cache_write, (cache, batch, pk, sk, pv, sv), device, stream, ())
 
@@ -491,7 +497,7 @@ def sparge_cache_read(k_pages, v_pages, page_table, first, cu, tokens: int, k_ex
     out = []
     for t, name in ((K, "K"), (V, "V")):
         if t is None:
-            t = torch.empty(shape, dtype=_BF16, device=device)
+            t = k_pages.new_empty(shape) if k_exp is None else torch.empty(shape, dtype=_BF16, device=device)
             made.append(t)
         else:
             _want(t, name, _BF16, shape, device)
@@ -511,7 +517,7 @@ def sparge_cache_attn(Q, k_pages, v_pages, page_table, first, cu_new, max_new: i
     pq, sq = _token_rows(Q, "Q", H, k_pages.shape[3], device)
     made = []
     if O is None:
-        O = torch.empty((T, H, d), dtype=_BF16, device=device)
+        O = Q.new_empty((T, H, d))
         made.append(O)
     else:
         _want(O, "O", _BF16, Q.shape, device)
@@ -520,7 +526,7 @@ def sparge_cache_attn(Q, k_pages, v_pages, page_table, first, cu_new, max_new: i
     n = 0
     if workspace is None:
         n = _lib.sparge_cache_attn_workspace_bytes(cache, batch, H, max_new, max_len, window)
-    ws, nws = _space(workspace, n, device, made)
+    ws, nws = _space(workspace, n, page_table, made)
     _launch(_lib.sparge_cache_attn, (cache, batch, pq, sq, H, max_new, max_len, window, O.data_ptr(), plse, ws, nws),
             device, stream, made)
     return O
