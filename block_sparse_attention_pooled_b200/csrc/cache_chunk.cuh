@@ -25,6 +25,11 @@ enum : unsigned int {
   kErrCcQ = 0xC00, kErrCcQEmpty, kErrCcKvFull, kErrCcKvEmpty, kErrCcS, kErrCcP, kErrCcO, kErrCcOFree, kErrCcDrain
 };
 
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // Waits for a phase for a millisecond at most, and says nothing.
 __device__ __forceinline__ void wait_quietly(uint32_t bar, uint32_t parity) {
   const unsigned long long t0 = globaltimer_ns();
@@ -407,15 +412,18 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
           for (int k = 0; k < U; ++k) {
             const int r = r0 + (k0 + k) * RS;
             const bool here = key0 + r < len && (there >> (r >> box_shift) & 1u);
-            const uint32_t power = here ? (e[k] == 255 ? 0x7FC0u : e[k] << 7) * 0x10001u : 0u;  // 2^e as bf16, twice
-            const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&power);
+            // 2^(e + 120) as bf16, twice; 2^120 and 2^e in two steps where that is out of range. 0: does not exist
+            // (the codes there may be anything, but as bf16 they are finite).
+            const bool far = here && e[k] > 134;
+            const uint32_t p1 = !here ? 0u : (e[k] == 255 ? 0x7FC0u : (far ? 247u : e[k] + 120u) << 7) * 0x10001u;
             const uint32_t w[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
             uint32_t v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t y = codes_to_bf16(__byte_perm(w[j / 2], 0, j & 1 ? 0x3424 : 0x1404));
-              const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), f);
-              v[j] = here ? *reinterpret_cast<const uint32_t*>(&z) : 0u;
+            for (int j = 0; j < 8; ++j)
+              v[j] = bf16x2_mul(codes_to_bf16(__byte_perm(w[j / 2], 0, j & 1 ? 0x4342 : 0x4140)), p1);
+            if (far) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] = bf16x2_mul(v[j], (e[k] << 7) * 0x10001u);
             }
             const uint32_t line = line0 + r * 128;
 #pragma unroll

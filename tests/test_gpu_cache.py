@@ -372,3 +372,21 @@ def test_output_at_any_16_bytes(sparge, new):
     want = sparge.sparge_cache_attn(*args)
     odd = torch.empty(Q.numel() + 8, dtype=torch.bfloat16, device="cuda")[8:].view(Q.shape)
     assert odd.data_ptr() % 32 == 16 and torch.equal(sparge.sparge_cache_attn(*args, O=odd), want)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_powers_at_both_ends(sparge, new):
+    """Keys so small and values so large (and the other way round) that their powers lie near the ends of the range."""
+    for ks, vs, qs in ((2.0 ** -60, 2.0 ** 60, 2.0 ** 60), (2.0 ** 40, 2.0 ** -40, 2.0 ** -40), (2.0 ** 10, 2.0 ** 100, 2.0 ** -10)):
+        c = Paged("e4m3", 2, 64, 32, [300])
+        k, v = c.normal(300, 2, 64) * ks, c.normal(300, 2, 64) * vs
+        first, cu = ints(0), ints(0, 300)
+        sparge.sparge_cache_write(k, v, c.k, c.v, c.table, first, cu, **c.exp)
+        k64, v64 = (e4m3_rows(x)[0].transpose(0, 1) for x in (k, v))
+        Q = c.normal(new, 4, 64) * qs
+        O = sparge.sparge_cache_attn(Q, c.k, c.v, c.table, ints(300 - new), ints(0, new), new, 300, **c.exp)
+        at = torch.arange(300, device="cuda")
+        seen = visible(at[-new:], at, 300, *CAUSAL)
+        for h in range(4):
+            o, _, to, _, _ = rows_fwd(Q[:, h], k64[h // 2], v64[h // 2], seen)
+            close(O[:, h], o, to, f"head {h}, keys {ks}")
