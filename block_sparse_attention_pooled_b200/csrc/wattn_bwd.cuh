@@ -43,6 +43,9 @@ struct WBwdParams {
   float scale_log2, scale;
 };
 
+// In place of D_i: the row sees a single key. (A NaN of no computation.)
+constexpr uint32_t kOneKey = 0x7FC05EE1u;
+
 // Rows [lo, hi) that see key j.
 __device__ __forceinline__ int key_row_lo(const Window& w, int j) {
   const int f = j / w.unit - w.right;
@@ -281,7 +284,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const int lo = p.w.lo(at), hi = p.w.hi(at, len);
     const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
     const int64_t row = (int64_t)bh * p.N + i;
-    const float nl2 = live ? -__ldg(p.lse + row) * 1.4426950408889634f : 0.0f;
+    // A row that sees a single key has P = 1 whatever its score, and a gradient of
+    // the score that is exactly 0 (dP - D would be rounding noise): its P is left
+    // out here (-inf), and a mark in place of D tells the other kernel.
+    const bool one = max(hi - lo, 0) + min(min(p.w.sinks, hi), lo) == 1;
+    const float nl2 = !live ? 0.0f : one ? -INFINITY : -__ldg(p.lse + row) * 1.4426950408889634f;
     // D_i in fp32, 16 rows per warp, a row's 16-byte pieces on neighbouring lanes.
     float* dots = reinterpret_cast<float*>(sgen + L::kOffDot);
     {
@@ -306,14 +313,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
         }
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane % LPR == 0) {
-          dots[r0 + u * RPS] = dot;
-          if (q0 + r0 + u * RPS < len) p.dsum[(int64_t)bh * p.N + q0 + r0 + u * RPS] = dot;
-        }
+        if (lane % LPR == 0) dots[r0 + u * RPS] = dot;
       }
     }
     asm volatile("bar.sync 2, 256;" ::: "memory");
     const float nd = -dots[r];
+    if (wg == 0 && live) p.dsum[row] = one ? __uint_as_float(kOneKey) : dots[r];
     const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), nl = f2(nl2, nl2), nd2 = f2(nd, nd);
     // Q and dO into TMEM, one by each group of warps.
     bool ok = true;
@@ -411,8 +416,8 @@ struct WDkvSmem {
   static constexpr int NS = D == 128 ? 5 : 8;
   static constexpr int kTileBytes = kWTile * D * 2;
   static constexpr int kOffK = 0, kOffV = kTileBytes, kOffRing = 2 * kTileBytes;
-  static constexpr int kOffVec = kOffRing + NS * kTileBytes;  // [2][128] fp32
-  static constexpr int kOffBar = kOffVec + 1024;
+  static constexpr int kOffVec = kOffRing + NS * kTileBytes;  // [2][128] fp32, then 128 bits
+  static constexpr int kOffBar = kOffVec + 1024 + 16;
   static constexpr int kBarKV = 0, kBarFull = 1, kBarEmpty = 1 + NS, kBarS = 1 + 2 * NS, kBarDp = 2 + 2 * NS,
                        kBarP = 3 + 2 * NS, kBarDs = 4 + 2 * NS, kBarVecFull = 5 + 2 * NS, kBarVecEmpty = 7 + 2 * NS,
                        kBarFinal = 9 + 2 * NS, kBarDrain = 10 + 2 * NS, kBarFix = 11 + 2 * NS;
@@ -568,13 +573,17 @@ __global__ void __launch_bounds__(kWThreads, 1)
     few_registers();
     int g = T > 0 ? t0 / nq : 0, qt = T > 0 ? t0 % nq : 0;
     float nl[4], nd[4];
+    uint32_t one[4];  // rows that see a single key
     auto fetch = [&] {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int i = row0 + qt * kWTile + 32 * k + lane;
         const int64_t row = (int64_t)(h0 + g) * p.N + i;
         nl[k] = i < len ? -__ldg(p.lse + row) * 1.4426950408889634f : -INFINITY;
-        nd[k] = i < len ? -__ldg(p.dsum + row) : 0.0f;
+        const float D_i = i < len ? __ldg(p.dsum + row) : 0.0f;
+        const bool mark = __float_as_uint(D_i) == kOneKey;
+        one[k] = __ballot_sync(0xffffffffu, mark);
+        nd[k] = mark ? 0.0f : -D_i;
       }
       if (++qt == nq) qt = 0, ++g;
     };
@@ -587,7 +596,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) vec[128 * h + 32 * k + lane] = h == 0 ? nl[k] : nd[k];
+          for (int k = 0; k < 4; ++k) {
+            vec[128 * h + 32 * k + lane] = h == 0 ? nl[k] : nd[k];
+            if (h == 1 && lane == k) reinterpret_cast<uint32_t*>(vec)[256 + k] = one[k];
+          }
         }
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(bar(L::kBarVecFull + h));
@@ -648,6 +660,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
       tc_fence_after();
       float dp[64];
       tmem_ld64(tmem + 128 + 64 * wg + lane_off, dp);
+      const uint2 one = *reinterpret_cast<const uint2*>(vec + 256 + 2 * wg);
+      if (one.x | one.y) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) s[i] = ((i < 32 ? one.x : one.y) >> (i % 32)) & 1u ? 0.0f : s[i];
+      }
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
         const float4 n4 = *reinterpret_cast<const float4*>(v + 128 + 4 * c);

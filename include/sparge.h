@@ -333,8 +333,9 @@ sparge_status sparge_window_fwd(const void* Q, const void* K, const void* V, con
  *   O, lse      the forward's, for the same inputs.
  *   dO          bf16 [B,H,N,d];  dQ: bf16 [B,H,N,d];  dK, dV: bf16 [B,Hkv,N,d].
  * Rows at or past L get zeros in dQ, dK and dV; what dO holds there does not
- * matter. Precision: fp32 scores, P and dS rounded to bf16 for their products,
- * fp32 sums, D_i from the bf16 O. No atomics: identical inputs give identical
+ * matter. A row that sees a single key has dS = 0 exactly. Precision: fp32
+ * scores, P and dS rounded to bf16 for their products, fp32 sums, D_i from the
+ * bf16 O. No atomics: identical inputs give identical
  * gradients. Workspace: sparge_window_workspace_bytes(SPARGE_OP_WINDOW_BWD, ...). */
 sparge_status sparge_window_bwd(const void* Q, const void* K, const void* V, const sparge_window_shape* shape,
                                 const sparge_window* window, const int32_t* lens, const void* O, const float* lse,

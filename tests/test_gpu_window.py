@@ -226,3 +226,17 @@ def test_a_row_of_nan_stays_a_row(sparge):
     assert torch.isnan(O[0, 0, 77]).all() and torch.isnan(lse[0, 0, 77])
     keep = torch.arange(300, device="cuda") != 77
     assert torch.equal(O[0, 0, keep], want[0, 0, keep]) and torch.equal(lse[0, 0, keep], clean[0, 0, keep])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,win", [(1, (-1, 0, 0, 1)), (1, (0, 0, 1, 5)), (300, (0, 0, 0, 1)), (5, (0, 0, 0, 1))])
+def test_rows_that_see_one_key_have_no_score_gradient(sparge, N, win, d):
+    """Their probability is 1 whatever the score: O is the key's v, dQ and dK are exactly 0, dV sums dO."""
+    Q, K, V, dO = inputs(2, 4, 2, N, d, seed=13)
+    lse = torch.empty(2, 4, N, device="cuda")
+    O = sparge.sparge_window_fwd(Q, K, V, *win[:2], sinks=win[2], unit=win[3], lse=lse)
+    dQ, dK, dV = sparge.sparge_window_bwd(Q, K, V, O, lse, dO, *win[:2], sinks=win[2], unit=win[3])
+    assert torch.equal(O, V.repeat_interleave(2, 1))
+    assert not dQ.any() and not dK.any()
+    want = dO.double().view(2, 2, 2, N, d).sum(2)
+    assert ((dV.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * dO.double().abs().amax()).all()
