@@ -148,8 +148,8 @@ template <int D>
 struct WDqSmem {
   static constexpr int NS = D == 128 ? 7 : 10;
   static constexpr int kTileBytes = kWTile * D * 2;
-  static constexpr int kOffDot = NS * kTileBytes;  // [128] fp32; Q and dO land in the last two slots first
-  static constexpr int kOffBar = kOffDot + 512;
+  static constexpr int kOffDot = NS * kTileBytes;  // [2][128] fp32; Q and dO land in the last two slots first
+  static constexpr int kOffBar = kOffDot + 1024;
   static constexpr int kBarIn = 0, kBarFull = 1, kBarEmpty = 1 + NS, kBarS = 1 + 2 * NS, kBarDp = 2 + 2 * NS,
                        kBarSFree = 3 + 2 * NS, kBarDs = 4 + 2 * NS, kBarTaken = 5 + 2 * NS, kBarFinal = 6 + 2 * NS,
                        kBarDrain = 7 + 2 * NS, kBarFix = 8 + 2 * NS;
@@ -183,6 +183,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
   KeyTiles kt{0, 0, 0, 0};
   if (q0 < len) kt = key_tiles(p.w.lo(q0), p.w.hi(min(q0 + kWTile, len) - 1, len), p.w.sinks, 0);
   const int T = kt.total;
+  // D_i comes from the forward's O, whose rounding to bf16 moves it by up to
+  // 2^-8 |dO_i| |O_i|: harmless where O_i is a mean of many values, but of the
+  // size of dS where a row sees few keys. So with few key tiles they are gone
+  // through twice, first for D_i = sum_j P_ij dP_ij in fp32. (With more than three
+  // tiles a row sees 256 keys or so.) 8 x 4000 rows, relative error of dQ: 2 keys
+  // 4.1e-3 -> 2.4e-3, 16 keys 2.8e-3 -> 2.4e-3, for 2 of 55 us a step.
+  const bool twice = T <= 3;
+  const int U = twice ? 2 * T : T;
+  auto key_of = [&](int u) { return kt.key0(u < T ? u : u - T); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) mbar_init(bar(i), i == L::kBarSFree || i == L::kBarDs || i == L::kBarTaken ? 256 : 1);
@@ -211,12 +220,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       FixUp fix{bar(L::kBarFix), 0};
       int n = 0;
-      for (; n < 2 * T; ++n) {  // K(0), V(0), K(1), ...
+      for (; n < 2 * U; ++n) {  // K(0), V(0), K(1), ...
         const int slot = n % NS;
         const bool ok = n == NS - 2 ? role_wait(bar(L::kBarTaken), 0, kErrWbIn, abort_flag)
                                     : n < NS || role_wait(bar(L::kBarEmpty + slot), (n / NS - 1) & 1, kErrWbEmpty, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) break;
-        if (!load_rows<D>(sKv + slot * L::kTileBytes, bar(L::kBarFull + slot), (n & 1) ? &tmV : &tmK, kt.key0(n >> 1),
+        if (!load_rows<D>(sKv + slot * L::kTileBytes, bar(L::kBarFull + slot), (n & 1) ? &tmV : &tmK, key_of(n >> 1),
                           len, p.N, kvh, lane, fix, abort_flag))
           break;
       }
@@ -235,8 +244,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
     auto slot = [&](int n) { return (uint64_t)(((n % NS) * L::kTileBytes) >> 4); };
     auto full = [&](int n) { return wait(L::kBarFull + n % NS, (n / NS) & 1, kErrWbFull); };
     bool ok = T > 0 && wait(L::kBarTaken, 0, kErrWbIn);
-    for (int t = -1; ok && t < T; ++t) {
-      const bool more = t + 1 < T;
+    for (int t = -1; ok && t < U; ++t) {
+      const bool more = t + 1 < U;
       const int k = 2 * (t + 1), v = k + 1;
       if (more) {
         ok = full(k) && (t < 0 || wait(L::kBarSFree, t & 1, kErrWbS));
@@ -253,7 +262,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-          mma_cols<D>(tmem + 256, tmem + 128, dKvM + slot(2 * t), t > 0);
+          if (t >= U - T) mma_cols<D>(tmem + 256, tmem + 128, dKvM + slot(2 * t), t > U - T);
           mma_commit(bar(L::kBarEmpty + (2 * t) % NS));
           if (!more) mma_commit(bar(L::kBarFinal));
         }
@@ -289,9 +298,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
     // out here (-inf), and a mark in place of D tells the other kernel.
     const bool one = max(hi - lo, 0) + min(min(p.w.sinks, hi), lo) == 1;
     const float nl2 = !live ? 0.0f : one ? -INFINITY : -__ldg(p.lse + row) * 1.4426950408889634f;
-    // D_i in fp32, 16 rows per warp, a row's 16-byte pieces on neighbouring lanes.
+    // dO_i . O_i in fp32, 16 rows per warp, a row's 16-byte pieces on neighbouring lanes.
     float* dots = reinterpret_cast<float*>(sgen + L::kOffDot);
-    {
+    if (!twice) {
       constexpr int LPR = D / 8, RPS = 32 / LPR, U = 16 / RPS;
       const int r0 = (warp - 4) * 16 + lane / LPR;
       const int64_t base = ((int64_t)bh * p.N + q0 + r0) * D + lane % LPR * 8;
@@ -316,10 +325,18 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (lane % LPR == 0) dots[r0 + u * RPS] = dot;
       }
     }
-    asm volatile("bar.sync 2, 256;" ::: "memory");
-    const float nd = -dots[r];
-    if (wg == 0 && live) p.dsum[row] = one ? __uint_as_float(kOneKey) : dots[r];
-    const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), nl = f2(nl2, nl2), nd2 = f2(nd, nd);
+    auto all_rows = [] { asm volatile("bar.sync 2, 256;" ::: "memory"); };
+    // The sum of both groups' shares of a row.
+    auto both = [&](float v) {
+      dots[128 * wg + r] = v;
+      all_rows();
+      return dots[r] + dots[128 + r];
+    };
+    all_rows();
+    float D_i = twice ? 0.0f : dots[r], more_D = 0.0f;
+    all_rows();
+    const uint64_t sc2 = f2(p.scale_log2, p.scale_log2), nl = f2(nl2, nl2);
+    uint64_t nd2 = f2(-D_i, -D_i);
     // Q and dO into TMEM, one by each group of warps.
     bool ok = true;
     if (T > 0) {
@@ -333,12 +350,18 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
     }
     const uint32_t ts = tmem + 64 * wg + lane_off, tp = tmem + 128 + 64 * wg + lane_off;
-    for (int t = 0; ok && t < T; ++t) {
-      const int key0 = kt.key0(t);
+    for (int u = 0; u < U; ++u) {
+      const int t = u < T ? u : u - T, key0 = kt.key0(t);
+      if (u == T) {  // the second time: D_i is known
+        D_i = both(more_D);
+        nd2 = f2(-D_i, -D_i);
+        more_D = 0.0f;
+      }
+      if (!ok) continue;
       const bool sink = t < kt.ns;
       const bool whole = sink ? key0 + kWTile <= min(kt.cut, all_hi) : key0 >= all_lo && key0 + kWTile <= all_hi;
-      ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarS), t & 1, kErrWbS, abort_flag));
-      if (!ok) break;
+      ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarS), u & 1, kErrWbS, abort_flag));
+      if (!ok) continue;
       tc_fence_after();
       float s[64], dp[64];
       tmem_ld64(ts, s);
@@ -360,20 +383,29 @@ __global__ void __launch_bounds__(kWThreads, 1)
           for (int j = 0; j < 32; ++j) s[32 * c + j] = (seen >> j) & 1u ? s[32 * c + j] : 0.0f;
         }
       }
-      ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarDp), t & 1, kErrWbDp, abort_flag));
-      if (!ok) break;
+      ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarDp), u & 1, kErrWbDp, abort_flag));
+      if (!ok) continue;
       tc_fence_after();
       tmem_ld64(tp, dp);
+      uint64_t sum = 0ull;  // of P dP (dP - 0) the first time, of dS the second: what D_i lacks
       uint32_t pk[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         const float2 g = f2_split(add2(f2(dp[2 * j], dp[2 * j + 1]), nd2));
-        pk[j] = pack_bf16x2(s[2 * j] * g.x, s[2 * j + 1] * g.y);
+        const float d0 = s[2 * j] * g.x, d1 = s[2 * j + 1] * g.y;
+        sum = add2(sum, f2(d0, d1));
+        pk[j] = pack_bf16x2(d0, d1);
       }
-      tmem_st32(tp, pk);
+      const float2 su = f2_split(sum);
+      more_D += su.x + su.y;
+      if (u >= U - T) tmem_st32(tp, pk);
       tc_fence_before();
       mbar_arrive(bar(L::kBarDs));
     }
+    // For the other kernel: D_i with what the sum of dS over the keys (0 but for
+    // D_i's error) says it lacks.
+    D_i += both(more_D);
+    if (wg == 0 && live) p.dsum[row] = one ? __uint_as_float(kOneKey) : D_i;
     if (ok && T > 0) {
       ok = __all_sync(0xffffffffu, role_wait(bar(L::kBarFinal), 0, kErrWbFinal, abort_flag));
       tc_fence_after();

@@ -240,3 +240,23 @@ def test_rows_that_see_one_key_have_no_score_gradient(sparge, N, win, d):
     assert not dQ.any() and not dK.any()
     want = dO.double().view(2, 2, 2, N, d).sum(2)
     assert ((dV.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * dO.double().abs().amax()).all()
+
+
+@pytest.mark.parametrize("win", [(1, 0, 0, 1), (3, 0, 4, 1), (0, 0, 0, 2), (30, 30, 0, 1)])
+def test_gradients_of_rows_that_see_few_keys(sparge, win):
+    """dS sums to 0 over a row's keys, and with few of them D's error does not average out: the relative error (2-norm)
+    of dQ and dK stays at what rounding dS and the result leaves, 2^-9 each in the mean of a uniform last bit times
+    sqrt(2): at most 2^-8 in all."""
+    Q, K, V, dO = inputs(1, 4, 2, 1500, 128, seed=14)
+    lse = torch.empty(1, 4, 1500, device="cuda")
+    O = sparge.sparge_window_fwd(Q, K, V, *win[:2], sinks=win[2], unit=win[3], lse=lse)
+    G = sparge.sparge_window_bwd(Q, K, V, O, lse, dO, *win[:2], sinks=win[2], unit=win[3])
+    at = torch.arange(1500, device="cuda")
+    seen = visible(at, at, 1500, *win)
+    dK = torch.zeros(2, 1500, 128, dtype=torch.float64, device="cuda")
+    for h in range(4):
+        o, _, to, P, _ = rows_fwd(Q[0, h], K[0, h // 2], V[0, h // 2], seen)
+        (dq, dk, _), _ = rows_bwd(Q[0, h], K[0, h // 2], V[0, h // 2], dO[0, h], P, o, to, seen)
+        assert (G[0][0, h].double() - dq).norm() <= 2.0 ** -8 * dq.norm()
+        dK[h // 2] += dk
+    assert (G[1][0].double() - dK).norm() <= 2.0 ** -8 * dK.norm()
