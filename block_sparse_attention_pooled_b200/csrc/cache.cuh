@@ -52,12 +52,13 @@ __device__ __forceinline__ int e4m3_power(float a) {
   return min(max(k - ((u & 0x7FFFFFu) > 0x600000u ? 7 : 8), -117), 119);
 }
 
-// Both kernels are bound by their bytes. One warp per token, so that the walk
-// from the packed token to its place (sequence, position, page: three loads
-// that wait for one another) is made once for all its 2 Hkv rows; a lane takes
-// 16 channels, 4 rows' (d = 128) or 8 rows' a step, four steps in flight.
-// 20 k tokens of 12 heads read back from e4m3: 67 us with a thread per 8
-// channels, 41 so (230 MB, 5.6 TB/s).
+// Both kernels are bound by their bytes. One warp per token and 16 (d = 128) or
+// 32 rows of its K and V heads, so that the walk from the packed token to its
+// place (sequence, position, page: three loads that wait for one another) is
+// made once for them; a lane takes 16 channels, four rows of each in flight.
+// 25 k tokens of 12 heads read back: from e4m3 67 us with a thread per 8
+// channels, 44 so (230 MB, two thirds of it written: 5.2 TB/s); from bf16 51 us
+// (6.0 TB/s).
 constexpr int kCacheWarps = 8;  // per block
 
 struct TokenPlace {
@@ -83,7 +84,8 @@ __global__ void __launch_bounds__(kCacheWarps * 32)
   const int t = blockIdx.x * kCacheWarps + threadIdx.x / 32;
   const TokenPlace at = token_place(c, t);
   if (!at.live || at.row < 0) return;
-  for (int r0 = 0; r0 < 2 * c.Hkv; r0 += U * RPS) {
+  {
+    const int r0 = blockIdx.y * (U * RPS);
     uint4 x[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -158,7 +160,8 @@ __global__ void __launch_bounds__(kCacheWarps * 32)
   const int t = blockIdx.x * kCacheWarps + threadIdx.x / 32;
   const TokenPlace at = token_place(c, t);
   if (!at.live) return;
-  for (int r0 = 0; r0 < 2 * c.Hkv; r0 += U * RPS) {
+  {
+    const int r0 = blockIdx.y * (U * RPS);
     uint4 x[U][2];
     uint8_t e[U];
 #pragma unroll

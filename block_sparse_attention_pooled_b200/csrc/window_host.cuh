@@ -340,7 +340,7 @@ sparge_status sparge_cache_write(const sparge_cache* cache, const sparge_cache_b
   if (!all_aligned16({K, V}) || k_stride < least || v_stride < least || k_stride % 8 || v_stride % 8)
     return SPARGE_ERR_INVALID_ARG;
   const __nv_bfloat16 *k = static_cast<const __nv_bfloat16*>(K), *vv = static_cast<const __nv_bfloat16*>(V);
-  const unsigned grid = (unsigned)ceil_div(batch->tokens, kCacheWarps);
+  const dim3 grid((unsigned)ceil_div(batch->tokens, kCacheWarps), (unsigned)ceil_div(2 * cache->Hkv, 4 * (cache->d == 64 ? 8 : 4)));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool q = cache->type == SPARGE_CACHE_E4M3;
   if (cache->d == 64) {
@@ -361,7 +361,7 @@ sparge_status sparge_cache_read(const sparge_cache* cache, const sparge_cache_ba
   if (batch->tokens == 0) return SPARGE_OK;
   if (!all_aligned16({K, V})) return SPARGE_ERR_INVALID_ARG;
   __nv_bfloat16 *k = static_cast<__nv_bfloat16*>(K), *vv = static_cast<__nv_bfloat16*>(V);
-  const unsigned grid = (unsigned)ceil_div(batch->tokens, kCacheWarps);
+  const dim3 grid((unsigned)ceil_div(batch->tokens, kCacheWarps), (unsigned)ceil_div(2 * cache->Hkv, 4 * (cache->d == 64 ? 8 : 4)));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool q = cache->type == SPARGE_CACHE_E4M3;
   if (cache->d == 64) {
