@@ -68,7 +68,7 @@ struct CacheItem {
   __device__ __forceinline__ void seq(const CacheAttnParams& p, int seq) {
     b = seq;
     const int end = min(__ldg(p.c.cu + b + 1), p.c.tokens);
-    cu = __ldg(p.c.cu + b);
+    cu = max(__ldg(p.c.cu + b), 0);
     n = max(end - cu, 0);
     first = max(__ldg(p.c.first + b), 0);
   }
@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(128) cache_combine_kernel(const CacheAttnParam
   const int4 own = p.owners[(int64_t)t * p.c.Hkv + h / p.G];
   const int c0 = own.x, c1 = own.z, r = own.w + h % p.G;
   if (c0 == c1) return;  // one CTA did it all
+  if (c0 < 0 || c0 > c1 || c1 >= p.ctas || r < 0 || r >= rows) return;  // never noted: the kernel before gave up a wait
   auto slot = [&](int c) { return (int64_t)(2 * c + (c == c0 ? own.y : 0)) * rows + r; };
   float m = -INFINITY;
   for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[slot(c)].x);

@@ -379,6 +379,7 @@ size_t sparge_cache_attn_workspace_bytes(const sparge_cache* cache, const sparge
   CacheView v;
   if (check_cache(cache, batch, &v) != SPARGE_OK) return 0;
   if (!window_ok(window) || H <= 0 || H % cache->Hkv || max_new < 1 || max_len < 1 || batch->tokens == 0) return 0;
+  if ((int64_t)batch->tokens * H > INT32_MAX || H / cache->Hkv > kWTile) return 0;
   return attn_plan(cache, batch, H, max_new).bytes;
 }
 

@@ -400,7 +400,8 @@ sparge_status sparge_cache_read(const sparge_cache* cache, const sparge_cache_ba
  *   O           bf16 [tokens, H, d], contiguous;  lse: optional float [tokens, H].
  * Precision as sparge_window_fwd; e4m3 rows enter the products as exact bf16.
  * A place of the cache that no position of the batch stands for may hold
- * anything, NaN too. Workspace: sparge_cache_attn_workspace_bytes(...). */
+ * anything, NaN too. Workspace: sparge_cache_attn_workspace_bytes(...), asked with
+ * the tensors' device current (0 if nothing is to be done or an argument is invalid). */
 size_t sparge_cache_attn_workspace_bytes(const sparge_cache* cache, const sparge_cache_batch* batch, int32_t H,
                                          int32_t max_new, int32_t max_len, const sparge_window* window);
 sparge_status sparge_cache_attn(const sparge_cache* cache, const sparge_cache_batch* batch, const void* Q,

@@ -390,3 +390,28 @@ def test_powers_at_both_ends(sparge, new):
         for h in range(4):
             o, _, to, _, _ = rows_fwd(Q[:, h], k64[h // 2], v64[h // 2], seen)
             close(O[:, h], o, to, f"head {h}, keys {ks}")
+
+
+def test_the_most_shared_heads(sparge):
+    attn_check(sparge, "bf16", 128, 1, 64, 16, [70, 5], [1, 3], CAUSAL)
+    attn_check(sparge, "e4m3", 100, 1, 128, 32, [150], [2], (40, 0, 3, 1))
+
+
+def test_a_shared_prefix(sparge):
+    """Two sequences whose tables begin with the same pages, and one sequence listed twice."""
+    c = Paged("bf16", 2, 64, 16, [100, 100])
+    ks, vs = c.fill(sparge, [100, 100])
+    c.table[1, :4] = c.table[0, :4]
+    k1, v1 = (torch.cat([x[0][:, :64], x[1][:, 64:]], 1) for x in (ks, vs))
+    table = torch.stack([c.table[0], c.table[1], c.table[0]])
+    for new in (1, 40):
+        q = c.normal(new, 4, 64)
+        Q = torch.cat([q, c.normal(new, 4, 64), q])
+        O = sparge.sparge_cache_attn(Q, c.k, c.v, table, ints(*[100 - new] * 3), ints(0, new, 2 * new, 3 * new), new, 100)
+        assert torch.equal(O[:new], O[2 * new:])
+        at = torch.arange(100, device="cuda")
+        seen = visible(at[-new:], at, 100, *CAUSAL)
+        for b, (kk, vv) in enumerate(((ks[0], vs[0]), (k1, v1))):
+            for h in range(4):
+                o, _, to, _, _ = rows_fwd(Q[b * new:(b + 1) * new, h], kk[h // 2], vv[h // 2], seen)
+                close(O[b * new:(b + 1) * new, h], o, to, f"sequence {b}, head {h}")

@@ -108,6 +108,21 @@ def test_cache_arguments(lib):
         assert attn(**k) == lib.ERR_INVALID_ARG, k
 
 
+def test_shared_heads_have_a_limit(lib):
+    """More than 128 query heads per K/V head: refused, and no workspace asked for (not a division by zero)."""
+    raw, w = lib.raw(), lib.Window(-1, 0, 0, 1)
+    c, b = cache(lib, Hkv=1), batch(lib, B=1, tokens=9)
+    for H in (129, 256, 100000):
+        assert raw.sparge_cache_attn(ref(c), ref(b), P, H * 128, H, 9, 100, ref(w), P, None, P, 1 << 40,
+                                     None) == lib.ERR_UNSUPPORTED
+        assert raw.sparge_cache_attn_workspace_bytes(ref(c), ref(b), H, 9, 100, ref(w)) == 0
+    assert raw.sparge_cache_attn_workspace_bytes(ref(c), ref(b), 128, 9, 100, ref(w)) > 0
+    for k in (dict(H=7, Hkv=2), dict(max_new=0), dict(max_len=0)):
+        a = dict(H=8, Hkv=2, max_new=1, max_len=10) | k
+        assert raw.sparge_cache_attn_workspace_bytes(ref(cache(lib, Hkv=a["Hkv"])), ref(b), a["H"], a["max_new"], a["max_len"],
+                                                     ref(w)) == 0
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
     q = torch.zeros(1, 2, 64, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
