@@ -2,7 +2,7 @@
 sparse + linear mix, as CUDA kernels for sm_100a behind a C ABI.
 
 The CUDA entry points live in :mod:`block_sparse_attention_pooled_b200.sparge`
-(importing it loads ``libsparge.so`` and fails loudly when it is missing).
+(importing it loads ``libsparge.so`` and ``_bind`` and fails loudly when one of them is missing).
 :mod:`block_sparse_attention_pooled_b200.synth` generates seeded inputs.
 """
 

@@ -1,10 +1,12 @@
-"""Builds libsparge.so in-tree with nvcc for sm_100a (one translation unit)."""
+"""Builds libsparge.so in-tree with nvcc for sm_100a (one translation unit), and the compiled binding of its newer
+entry points, _bind, against it and torch."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -13,6 +15,8 @@ HEADERS = [os.path.join(PKG, "csrc", f) for f in ("ptx.cuh", "mask.cuh", "attn.c
     os.path.join(ROOT, "include", "sparge.h")
 ]
 LIB = os.path.join(PKG, "libsparge.so")
+BIND_SRC = os.path.join(PKG, "csrc", "bind.cpp")
+BIND = os.path.join(PKG, "_bind" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -43,7 +47,29 @@ def build(force: bool = False, verbose: bool = False) -> str:
             cmd.insert(1, "-Xptxas=-v")
         subprocess.check_call(cmd, stdout=None if verbose else subprocess.DEVNULL)
         os.replace(tmp, LIB)
+    deps = [BIND_SRC, os.path.join(ROOT, "include", "sparge.h")]
+    if force or not os.path.exists(BIND) or any(os.path.getmtime(f) > os.path.getmtime(BIND) for f in deps):
+        _build_bind()
     return LIB
+
+
+def _build_bind() -> None:
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    lib = os.path.join(base, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    tmp = BIND + f".tmp{os.getpid()}"
+    subprocess.check_call([
+        shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-DTORCH_EXTENSION_NAME=_bind",
+        "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(base, "include"),
+        "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+        "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, BIND_SRC, "-o", tmp,
+        "-L", PKG, "-l:libsparge.so", "-Wl,-rpath,$ORIGIN",
+        "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python",
+    ])
+    os.replace(tmp, BIND)
 
 
 if __name__ == "__main__":

@@ -1,7 +1,8 @@
 """Python binding of the C ABI in include/sparge.h (argument marshalling only).
 
-Importing this module loads ``libsparge.so`` from the package directory and
-raises ImportError when it is missing: there is no fallback implementation.
+Importing this module loads ``libsparge.so`` and the compiled binding ``_bind``
+from the package directory and raises ImportError when one of them is missing:
+there is no fallback implementation.
 Tensors are torch CUDA tensors; every call is enqueued on the current torch
 stream (or the stream given) and returns without synchronising.
 """
@@ -10,7 +11,6 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-import struct
 from typing import Optional, Tuple
 
 import torch
@@ -19,6 +19,11 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsparge.
 if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{_LIB_PATH} is missing: build it with `python -m block_sparse_attention_pooled_b200.build`")
 _lib = ctypes.CDLL(_LIB_PATH)
+try:
+    from . import _bind
+except ImportError as e:
+    raise ImportError(f"_bind is missing or was built for another torch: rebuild it with "
+                      f"`python -m block_sparse_attention_pooled_b200.build --force` ({e})") from e
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_TIMEOUT = range(6)
 OP_MASK, OP_ATTN, OP_SLA2, OP_ATTN_Q8, OP_MASK_ROUTER, OP_ATTN_BWD, OP_SLA2_BWD = 0, 1, 2, 3, 4, 5, 6
@@ -330,58 +335,14 @@ def device_status(stream=None) -> int:
 
 # ---------------------------------------------------------------------------
 # Windowed attention and the paged cache. A single token's call takes a few
-# microseconds on the GPU, so these bindings look at each argument once, pack
-# the C structs in one go and hand plain addresses over.
+# microseconds on the GPU, so the arguments are checked in compiled code
+# (csrc/bind.cpp); what is here are the names, the defaults and what they do.
 # ---------------------------------------------------------------------------
-_pack_wshape = struct.Struct("5i").pack
-_pack_window = struct.Struct("4i").pack
-_pack_cache = struct.Struct("4P5i4x").pack
-_pack_batch = struct.Struct("3P3i4x").pack
-_BF16, _F32, _I32, _U8, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.float8_e4m3fn
+_bind.set_error(SpargeError)
 
 
-_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-# The current stream's handle without an object for it.
-_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _launch(fn, args, device, stream, made):
-    """Calls fn(*args, stream handle) with the tensors' device current. `made`: tensors taken here; on a stream that is
-    not the current one, their memory is not handed out again before that stream is done with them."""
-    index = device.index
-    handle = _current_handle(index)
-    if stream is not None:
-        if stream.device.index != index:
-            raise ValueError("the stream belongs to another device than the tensors")
-        if stream.cuda_stream != handle:
-            handle = stream.cuda_stream
-            for t in made:
-                t.record_stream(stream)
-    if _get_device() == index:
-        rc = fn(*args, handle)
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, handle)
-    if rc:
-        raise SpargeError(rc, fn.__name__)
-
-
-def _want(t, name, dtype, shape, device):
-    if t.dtype is not dtype or t.get_device() != device.index or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}")
-    return t.data_ptr()
-
-
-def _window_args(Q, K, V, left, right, sinks, unit, lens):
-    qs, ks, device = Q.shape, K.shape, Q.device
-    index = device.index
-    if (Q.dtype is not _BF16 or K.dtype is not _BF16 or V.dtype is not _BF16 or not Q.is_cuda or len(qs) != 4
-            or len(ks) != 4 or ks != V.shape or ks[0] != qs[0] or ks[2:] != qs[2:] or K.get_device() != index
-            or V.get_device() != index or not Q.is_contiguous() or not K.is_contiguous() or not V.is_contiguous()):
-        raise ValueError("Q, K, V must be contiguous bf16 CUDA tensors of shape [B,H,N,d] and [B,Hkv,N,d]")
-    B, H, N, d = qs
-    plens = None if lens is None else _want(lens, "lens", _I32, (B,), device)
-    return _pack_wshape(B, H, ks[1], N, d), _pack_window(left, right, sinks, unit), plens, device
+def _on(stream):
+    return None if stream is None else (stream.device.index, stream.cuda_stream)
 
 
 def sparge_window_fwd(Q, K, V, left: int, right: int, sinks: int = 0, unit: int = 1, lens=None, O=None, lse=None,
@@ -389,121 +350,24 @@ def sparge_window_fwd(Q, K, V, left: int, right: int, sinks: int = 0, unit: int 
     """Attention with a sliding window and sinks over [B,H,N,d] (K, V: [B,Hkv,N,d]); left and right count units of
     `unit` tokens, -1 for no limit; lens: int32 [B] lengths of a padded batch. Returns O (and fills lse if given).
     It needs no workspace."""
-    shape, window, plens, device = _window_args(Q, K, V, left, right, sinks, unit, lens)
-    made = ()
-    if O is None:
-        O = torch.empty_like(Q)
-        made = (O,)
-    else:
-        _want(O, "O", _BF16, Q.shape, device)
-    plse = None if lse is None else _want(lse, "lse", _F32, Q.shape[:3], device)
-    _launch(_lib.sparge_window_fwd, (Q.data_ptr(), K.data_ptr(), V.data_ptr(), shape, window, plens, O.data_ptr(), plse,
-                                     None, 0), device, stream, made)
-    return O
-
-
-def _space(workspace, n, like, made):
-    """Address and bytes of the workspace: the caller's, or n bytes taken here, as `like`'s type, and added to `made`."""
-    if workspace is None:
-        if n == 0:
-            return None, 0
-        workspace = like.new_empty(-(-n // like.element_size()))
-        made.append(workspace)
-        return workspace.data_ptr(), n
-    if workspace.device != like.device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return _bind.window_fwd(Q, K, V, left, right, sinks, unit, lens, O, lse, _on(stream))
 
 
 def sparge_window_bwd(Q, K, V, O, lse, dO, left: int, right: int, sinks: int = 0, unit: int = 1, lens=None, dQ=None,
                       dK=None, dV=None, workspace=None, stream=None):
     """Gradients of sparge_window_fwd (O and lse from that call) for dL/dO = dO. Returns (dQ, dK, dV)."""
-    shape, window, plens, device = _window_args(Q, K, V, left, right, sinks, unit, lens)
-    pO, pdO = _want(O, "O", _BF16, Q.shape, device), _want(dO, "dO", _BF16, Q.shape, device)
-    plse = _want(lse, "lse", _F32, Q.shape[:3], device)
-    made = []
-    out = []
-    for t, like, name in ((dQ, Q, "dQ"), (dK, K, "dK"), (dV, V, "dV")):
-        if t is None:
-            t = torch.empty_like(like)
-            made.append(t)
-        else:
-            _want(t, name, _BF16, like.shape, device)
-        out.append(t)
-    n = _lib.sparge_window_workspace_bytes(OP_WINDOW_BWD, shape, window) if workspace is None else 0
-    ws, nws = _space(workspace, n, lse, made)
-    _launch(_lib.sparge_window_bwd, (Q.data_ptr(), K.data_ptr(), V.data_ptr(), shape, window, plens, pO, plse, pdO,
-                                     out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), ws, nws), device, stream,
-            made)
-    return tuple(out)
-
-
-def _cache_args(k_pages, v_pages, k_exp, v_exp, page_table, first, cu, tokens):
-    """The two C structs of a paged cache and a batch of its sequences, and the device."""
-    device, dtype, shape = k_pages.device, k_pages.dtype, k_pages.shape
-    index = device.index
-    if (not k_pages.is_cuda or len(shape) != 4 or v_pages.dtype is not dtype or v_pages.shape != shape
-            or v_pages.get_device() != index or not k_pages.is_contiguous() or not v_pages.is_contiguous()):
-        raise ValueError("the cache's pages must be contiguous CUDA tensors of one type and of shape [pages, Hkv, page, d]")
-    if dtype is _BF16:
-        kind, ek, ev = CACHE_BF16, 0, 0
-        if k_exp is not None or v_exp is not None:
-            raise ValueError("a bf16 cache has no exponents")
-    elif dtype is _E4M3:
-        if k_exp is None or v_exp is None:
-            raise ValueError("an e4m3 cache needs k_exp and v_exp")
-        kind = CACHE_E4M3
-        ek, ev = _want(k_exp, "k_exp", _U8, shape[:3], device), _want(v_exp, "v_exp", _U8, shape[:3], device)
-    else:
-        raise ValueError("a cache holds bfloat16 or float8_e4m3fn")
-    table = page_table.shape
-    B = table[0] if len(table) == 2 else -1
-    if (B < 0 or page_table.dtype is not _I32 or first.dtype is not _I32 or cu.dtype is not _I32 or first.shape != (B,)
-            or cu.shape != (B + 1,) or page_table.get_device() != index or first.get_device() != index
-            or cu.get_device() != index or not page_table.is_contiguous() or not first.is_contiguous()
-            or not cu.is_contiguous()):
-        raise ValueError(f"page_table [B, max_pages], first [B] and cu [B + 1] must be contiguous int32 tensors on {device}")
-    return (_pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), ek, ev, *shape, kind),
-            _pack_batch(page_table.data_ptr(), first.data_ptr(), cu.data_ptr(), B, table[1], tokens), device)
-
-
-def _token_rows(t, name, heads, d, device):
-    """Address and token stride of packed tokens [T, heads, d]: heads and channels contiguous, tokens any stride."""
-    shape, stride = t.shape, t.stride()
-    if (t.dtype is not _BF16 or t.get_device() != device.index or len(shape) != 3 or shape[1] != heads or shape[2] != d
-            or (shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != d)))):
-        raise ValueError(f"{name} must be a bf16 tensor of shape [tokens, {heads}, {d}] on {device}, contiguous within a token")
-    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * d
+    return _bind.window_bwd(Q, K, V, O, lse, dO, left, right, sinks, unit, lens, dQ, dK, dV, workspace, _on(stream))
 
 
 def sparge_cache_write(k, v, k_pages, v_pages, page_table, first, cu_new, k_exp=None, v_exp=None, stream=None) -> None:
     """Writes new tokens' k, v (bf16 [T,Hkv,d], any token stride) into the paged cache at positions first[b], ..."""
-    T = k.shape[0]
-    cache, batch, device = _cache_args(k_pages, v_pages, k_exp, v_exp, page_table, first, cu_new, T)
-    _, Hkv, _, d = k_pages.shape
-    pk, sk = _token_rows(k, "k", Hkv, d, device)
-    pv, sv = _token_rows(v, "v", Hkv, d, device)
-    if v.shape[0] != T:
-        raise ValueError("k and v must hold the same tokens")
-    _launch(_lib.sparge_cache_write, (cache, batch, pk, sk, pv, sv), device, stream, ())
+    _bind.cache_write(k, v, k_pages, v_pages, page_table, first, cu_new, k_exp, v_exp, _on(stream))
 
 
 def sparge_cache_read(k_pages, v_pages, page_table, first, cu, tokens: int, k_exp=None, v_exp=None, K=None, V=None,
                       stream=None):
     """The batch's positions first[b], ... (cu[b+1] - cu[b] of them, `tokens` rows in all) as bf16 (K, V) [tokens,Hkv,d]."""
-    cache, batch, device = _cache_args(k_pages, v_pages, k_exp, v_exp, page_table, first, cu, tokens)
-    shape = (tokens, k_pages.shape[1], k_pages.shape[3])
-    made = []
-    out = []
-    for t, name in ((K, "K"), (V, "V")):
-        if t is None:
-            t = k_pages.new_empty(shape) if k_exp is None else torch.empty(shape, dtype=_BF16, device=device)
-            made.append(t)
-        else:
-            _want(t, name, _BF16, shape, device)
-        out.append(t)
-    _launch(_lib.sparge_cache_read, (cache, batch, out[0].data_ptr(), out[1].data_ptr()), device, stream, made)
-    return out[0], out[1]
+    return _bind.cache_read(k_pages, v_pages, page_table, first, cu, tokens, k_exp, v_exp, K, V, _on(stream))
 
 
 def sparge_cache_attn(Q, k_pages, v_pages, page_table, first, cu_new, max_new: int, max_len: int, left: int = -1,
@@ -512,21 +376,5 @@ def sparge_cache_attn(Q, k_pages, v_pages, page_table, first, cu_new, max_new: i
     """Attention of the new tokens Q (bf16 [T,H,d], any token stride), which stand at positions first[b], ... of their
     sequences, over the paged cache that holds those positions already. max_new and max_len bound a sequence's new
     tokens and its length. Returns O [T,H,d] (and fills lse [T,H] if given)."""
-    T, H, d = Q.shape
-    cache, batch, device = _cache_args(k_pages, v_pages, k_exp, v_exp, page_table, first, cu_new, T)
-    pq, sq = _token_rows(Q, "Q", H, k_pages.shape[3], device)
-    made = []
-    if O is None:
-        O = Q.new_empty((T, H, d))
-        made.append(O)
-    else:
-        _want(O, "O", _BF16, Q.shape, device)
-    plse = None if lse is None else _want(lse, "lse", _F32, (T, H), device)
-    window = _pack_window(left, right, sinks, unit)
-    n = 0
-    if workspace is None:
-        n = _lib.sparge_cache_attn_workspace_bytes(cache, batch, H, max_new, max_len, window)
-    ws, nws = _space(workspace, n, page_table, made)
-    _launch(_lib.sparge_cache_attn, (cache, batch, pq, sq, H, max_new, max_len, window, O.data_ptr(), plse, ws, nws),
-            device, stream, made)
-    return O
+    return _bind.cache_attn(Q, k_pages, v_pages, page_table, first, cu_new, max_new, max_len, left, right, sinks, unit,
+                            k_exp, v_exp, O, lse, workspace, _on(stream))
