@@ -119,19 +119,33 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+// A tiled map of `rank` dimensions (innermost first), zero fill outside the
+// tensor. The driver's call needs a current context, which a host thread has
+// only after its first runtime call that takes one: then it is taken, and the
+// map made again.
+bool encode_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  for (int attempt = 0;; ++attempt) {
+    const CUresult r = fn(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    int dev = 0;
+    if (r != CUDA_ERROR_INVALID_CONTEXT || attempt > 0 || cudaGetDevice(&dev) != cudaSuccess ||
+        cudaSetDevice(dev) != cudaSuccess)
+      return r == CUDA_SUCCESS;
+  }
+}
+
 // 3-D bf16 map over [BH][N][d] with a (64 columns x rows x 1) box, 128-byte
 // swizzle, zero fill outside the tensor.
 bool make_map_bhnd(CUtensorMap* m, const void* base, int64_t BH, int N, int d, int box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)N, (cuuint64_t)BH};
   cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)N * d * 2};
   cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Raises a kernel's dynamic shared memory limit once per device. Any host
@@ -249,16 +263,10 @@ sparge_status launch_mask(const void* Q, const void* K, const sparge_shape* s, c
 // 3-D map over one-byte codes [BH][N][128] with a (128 x rows x 1) box,
 // 128-byte swizzle, zero fill outside the tensor.
 bool make_map_u8(CUtensorMap* m, const void* base, int64_t BH, int N, int box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
   cuuint64_t dims[3] = {128, (cuuint64_t)N, (cuuint64_t)BH};
   cuuint64_t strides[2] = {128, (cuuint64_t)N * 128};
   cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Workspace of the backward: D_i per row, the transposed mask (query-block

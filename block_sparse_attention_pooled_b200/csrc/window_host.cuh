@@ -233,31 +233,21 @@ AttnPlan attn_plan(const sparge_cache* c, const sparge_cache_batch* b, int32_t H
 int box_rows(const sparge_cache* c) { return std::min(c->page, c->type == SPARGE_CACHE_E4M3 ? 128 : 64); }
 
 bool make_map_pages(CUtensorMap* m, const void* base, const sparge_cache* c) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
   const bool q = c->type == SPARGE_CACHE_E4M3;
   const cuuint64_t width = q ? 1 : 2;
   cuuint64_t dims[3] = {(cuuint64_t)c->d, (cuuint64_t)c->page, (cuuint64_t)c->pages * c->Hkv};
   cuuint64_t strides[2] = {c->d * width, (cuuint64_t)c->page * c->d * width};
   cuuint32_t box[3] = {q ? (cuuint32_t)c->d : 64, (cuuint32_t)box_rows(c), 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, q ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            q && c->d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(m, q ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
+                    q && c->d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Q as [Hkv][tokens][G][d] with (64 channels x G heads x tq tokens) boxes.
 bool make_map_q(CUtensorMap* m, const CacheAttnParams& p, int d, int tq) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
   cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)p.G, (cuuint64_t)p.c.tokens, (cuuint64_t)p.c.Hkv};
   cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)p.q_stride * 2, (cuuint64_t)p.G * d * 2};
   cuuint32_t box[4] = {64, (cuuint32_t)p.G, (cuuint32_t)tq, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<__nv_bfloat16*>(p.Q), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p.Q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int D, bool E4M3, int R8>

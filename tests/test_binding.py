@@ -1,4 +1,6 @@
 """What the compiled binding of the windowed and cached entry points refuses by itself, before the C ABI sees it."""
+import threading
+
 import pytest
 import torch
 
@@ -139,3 +141,26 @@ def test_cache_tensors(lib):
     with pytest.raises(lib.SpargeError) as e:
         lib.sparge_cache_attn(Q, pages, pages, table, first, cu, 0, 32)
     assert e.value.code == lib.ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+def test_threads_call_at_once(lib):
+    """Four threads, each with its own stream: the same results as one after the other."""
+    ins = [window_inputs(N=100 + 37 * i) for i in range(4)]
+    want = [lib.sparge_window_fwd(*t, 20, 0) for t in ins]
+    torch.cuda.synchronize()
+    got = [[] for _ in ins]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for _ in range(50):
+            got[i].append(lib.sparge_window_fwd(*ins[i], 20, 0, stream=s))
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(4):
+        assert len(got[i]) == 50 and all(torch.equal(o, want[i]) for o in got[i])
