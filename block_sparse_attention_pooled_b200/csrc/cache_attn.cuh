@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
     fence_mbar_init();
   }
   __syncthreads();
+  grid_let_next();
   const int64_t W = count_units<KT>(p, lane);
   const int ctas = ctas_used(W, p.ctas);
   if ((int)blockIdx.x >= ctas) return;

@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_let_next();
   const int tq = p.tpt / 2;  // tokens per 128-row tile
 
   // This CTA's run of units.

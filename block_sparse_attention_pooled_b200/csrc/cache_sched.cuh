@@ -243,6 +243,7 @@ __device__ __forceinline__ int run_owner(int64_t W, int ctas, int64_t u) {
 // token's rows lie in, if there is more than one. rows: of a partial.
 template <int D>
 __global__ void __launch_bounds__(128) cache_combine_kernel(const CacheAttnParams p, int rows) {
+  grid_wait();
   constexpr int C = D / 32;  // neighbouring channels per lane
   const int lane = threadIdx.x % 32;
   const int64_t id = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;

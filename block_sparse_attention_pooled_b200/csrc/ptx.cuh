@@ -377,4 +377,12 @@ __device__ __forceinline__ float phi_elu1(float x) {
   return x > 0.0f ? x + 1.0f : e;
 }
 
+// A kernel may let the next one in its stream start early (once all its blocks
+// have said so or ended); that one, launched with the attribute for it, goes on
+// past grid_wait() when this one is over and its writes are visible. Every
+// thread that ends has to have passed grid_wait() first, or a third kernel
+// could start before the first is over.
+__device__ __forceinline__ void grid_let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 }  // namespace sparge

@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_let_next();
   auto few_registers = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); };
 
   if (warp == 0) {
@@ -513,6 +514,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_wait();  // for D_i
+  grid_let_next();
   auto few_registers = [] { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); };
 
   if (warp == 0) {
@@ -612,7 +615,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const int i = row0 + qt * kWTile + 32 * k + lane;
         const int64_t row = (int64_t)(h0 + g) * p.N + i;
         nl[k] = i < len ? -__ldg(p.lse + row) * 1.4426950408889634f : -INFINITY;
-        const float D_i = i < len ? __ldg(p.dsum + row) : 0.0f;
+        const float D_i = i < len ? __ldcg(p.dsum + row) : 0.0f;
         const bool mark = __float_as_uint(D_i) == kOneKey;
         one[k] = __ballot_sync(0xffffffffu, mark);
         nd[k] = mark ? 0.0f : -D_i;
@@ -747,6 +750,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
 // thread per four channels of a (K/V head, tile, which, key).
 template <int D>
 __global__ void __launch_bounds__(256) window_reduce_kernel(const WBwdParams p, int64_t quads) {
+  grid_wait();
   constexpr int QD = D / 4;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= quads) return;

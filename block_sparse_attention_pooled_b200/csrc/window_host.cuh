@@ -33,6 +33,26 @@ bool all_aligned16(std::initializer_list<const void*> ps) {
   return true;
 }
 
+// Launches a kernel that waits itself (grid_wait) for the one before it in the
+// stream, which this call launched: its blocks start, and get ready, while that
+// one's last blocks still run.
+template <typename... Params, typename... Args>
+cudaError_t launch_next(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+                        const Args&... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  cudaLaunchKernelEx(&c, kernel, Params(args)...);
+  return cudaGetLastError();
+}
+
 // How the rows of dK and dV's key tiles are split, from what the host knows.
 // A key that every later row sees (a sink, or any key where the past is not
 // limited) has up to N rows per head, another as many as the window is wide;
@@ -158,15 +178,17 @@ sparge_status launch_window_bwd(const void* Q, const void* K, const void* V, con
   cudaError_t e = ensure_smem(window_dq_kernel<D>, WDqSmem<D>::kBytes, D == 64 ? 22 : 23);
   if (e != cudaSuccess) return cuda_status(e);
   window_dq_kernel<D><<<(unsigned)gq, kWThreads, WDqSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_status(e);
   e = ensure_smem(window_dkdv_kernel<D>, WDkvSmem<D>::kBytes, D == 64 ? 24 : 25);
   if (e != cudaSuccess) return cuda_status(e);
-  window_dkdv_kernel<D><<<(unsigned)gk, kWThreads, WDkvSmem<D>::kBytes, st>>>(mq, mk, mv, mdo, p);
-  if (k.slots > 0) {
+  e = launch_next(window_dkdv_kernel<D>, (unsigned)gk, kWThreads, WDkvSmem<D>::kBytes, st, mq, mk, mv, mdo, p);
+  if (e == cudaSuccess && k.slots > 0) {
     const int64_t quads = dm.BHkv * k.tiles * 2 * kWTile * (D / 4);
     if (ceil_div(quads, 256) > INT32_MAX) return SPARGE_ERR_UNSUPPORTED;
-    window_reduce_kernel<D><<<(unsigned)ceil_div(quads, 256), 256, 0, st>>>(p, quads);
+    e = launch_next(window_reduce_kernel<D>, (unsigned)ceil_div(quads, 256), 256, 0, st, p, quads);
   }
-  return cuda_status(cudaGetLastError());
+  return cuda_status(e);
 }
 
 // ---------------------------------------------------------------- paged cache
@@ -268,8 +290,7 @@ sparge_status launch_cache_attn(const sparge_cache* c, const CacheAttnParams& p,
   if (plan.rows <= 16) {
     e = plan.rows == 8 ? launch_decode<D, E4M3, 1>(mk, mv, p, st) : launch_decode<D, E4M3, 2>(mk, mv, p, st);
     if (e != cudaSuccess) return cuda_status(e);
-    cache_combine_kernel<D><<<join, 128, 0, st>>>(p, plan.rows);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_next(cache_combine_kernel<D>, join, 128, 0, st, p, plan.rows));
   }
   CUtensorMap mq;
   if (!make_map_q(&mq, p, D, plan.tpt / 2)) return SPARGE_ERR_CUDA;
@@ -278,8 +299,7 @@ sparge_status launch_cache_attn(const sparge_cache* c, const CacheAttnParams& p,
   cache_chunk_kernel<D, E4M3><<<p.ctas, chunk_threads<E4M3>(), ChunkSmem<D, E4M3>::kBytes, st>>>(mq, mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e);
-  cache_combine_kernel<D><<<join, 128, 0, st>>>(p, plan.rows);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(launch_next(cache_combine_kernel<D>, join, 128, 0, st, p, plan.rows));
 }
 
 }  // namespace
