@@ -158,13 +158,15 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
   }
   __syncthreads();
   grid_let_next();
-  const int64_t W = count_units<KT>(p, lane);
-  const int ctas = ctas_used(W, p.ctas);
-  if ((int)blockIdx.x >= ctas) return;
-  const int64_t start = run_start(W, ctas, blockIdx.x), end = run_start(W, ctas, blockIdx.x + 1);
-  int at;
-  CacheItem<KT> it = find_unit<KT>(p, start, lane, at);
-  int64_t left = end - start;
+  CacheRun<KT> run;
+  run.find(p, blockIdx.x, lane);
+  if (run.left == 0) return;
+  const int64_t W = run.W;
+  const int ctas = run.ctas;
+  CacheItem<KT> it = run.it;
+  int at = run.at;
+  const int64_t start = run.start, end = start + run.left;
+  int64_t left = run.left;
 
   if (warp >= NW) {
     // ------------------------------------------------------------ producers: one warp for K, one for V

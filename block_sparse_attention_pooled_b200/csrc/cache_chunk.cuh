@@ -98,14 +98,15 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
   const int tq = p.tpt / 2;  // tokens per 128-row tile
 
   // This CTA's run of units.
-  const int64_t W = count_units<KT>(p, lane);
-  const int ctas = ctas_used(W, p.ctas);
-  const bool work = (int)blockIdx.x < ctas;
-  const int64_t start = work ? run_start(W, ctas, blockIdx.x) : 0, end = work ? run_start(W, ctas, blockIdx.x + 1) : 0;
-  int at = 0;
-  CacheItem<KT> it;
-  if (work) it = find_unit<KT>(p, start, lane, at);
-  int64_t left = end - start;
+  CacheRun<KT> run;
+  run.find(p, blockIdx.x, lane);
+  const int64_t W = run.W;
+  const int ctas = run.ctas;
+  const bool work = run.left > 0;
+  CacheItem<KT> it = run.it;
+  int at = run.at;
+  const int64_t start = run.start, end = start + run.left;
+  int64_t left = run.left;
   auto few_registers = [] {
     if (E4M3) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");

@@ -78,6 +78,16 @@ struct CacheItem {
     kt = key_tiles_of<KT>(p.w.lo(first + t0), p.w.hi(first + t1, len()), p.w.sinks, (1 << p.c.page_shift) - 1);
     T = max(kt.total, 1);
   }
+  // Unit `in` of the row tile's: its K/V head, and its place there.
+  __device__ __forceinline__ void place(int64_t in, int& at) {
+    if (in < INT32_MAX) {
+      hk = (int)in / T;
+      at = (int)in - hk * T;
+    } else {
+      hk = (int)(in / T);
+      at = (int)(in % T);
+    }
+  }
   // To the next item; false past the last.
   __device__ __forceinline__ bool next(const CacheAttnParams& p) {
     if (++hk < p.c.Hkv) return true;
@@ -140,20 +150,7 @@ __device__ __forceinline__ void walk_tiles(const CacheAttnParams& p, int lane, F
   }
 }
 
-// Units of all items.
-template <int KT>
-__device__ __forceinline__ int64_t count_units(const CacheAttnParams& p, int lane) {
-  int64_t total = 0;
-  walk_tiles<KT>(p, lane, [&](const CacheItem<KT>& x) {
-    total += x.T;
-    return false;
-  });
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  return total * p.c.Hkv;
-}
-
-// The item that holds unit u (u < count_units) and u's place in it. Called by a whole warp.
+// The item that holds unit u (below their number) and u's place in it. Called by a whole warp.
 template <int KT>
 __device__ __forceinline__ CacheItem<KT> find_unit(const CacheAttnParams& p, int64_t u, int lane, int& at) {
   int64_t base = 0;
@@ -181,14 +178,7 @@ __device__ __forceinline__ CacheItem<KT> find_unit(const CacheAttnParams& p, int
     return true;
   });
   found.keys(p);
-  const int64_t in = u - base;
-  if (in < INT32_MAX) {
-    found.hk = (int)in / found.T;
-    at = (int)in - found.hk * found.T;
-  } else {
-    found.hk = (int)(in / found.T);
-    at = (int)(in % found.T);
-  }
+  found.place(u - base, at);
   return found;
 }
 
@@ -238,6 +228,66 @@ __device__ __forceinline__ int64_t run_start(int64_t W, int ctas, int c) {
 __device__ __forceinline__ int run_owner(int64_t W, int ctas, int64_t u) {
   return W < (1 << 20) ? (int)(((uint32_t)(u + 1) * (uint32_t)ctas - 1) / (uint32_t)W) : (int)(((u + 1) * ctas - 1) / W);
 }
+
+// CTA `cta`'s run: its first unit's item, that unit's place in it, and the
+// units (0: none). ctas: the CTAs that get a run. Called by a whole warp. Up to
+// 32 row tiles are gone through once (counting them and searching them in two
+// walks took 2 us more, of 12 for one token of one stream); more take both.
+template <int KT>
+struct CacheRun {
+  CacheItem<KT> it;
+  int at, ctas;
+  int64_t W, start, left;
+
+  __device__ __forceinline__ void find(const CacheAttnParams& p, int cta, int lane) {
+    CacheItem<KT> x;
+    int rounds = 0;
+    int64_t total = 0;
+    x.T = 0;
+    walk_tiles<KT>(p, lane, [&](const CacheItem<KT>& y) {
+      total += y.T;
+      if (y.T) x = y;
+      ++rounds;
+      return false;
+    });
+    at = 0;
+    if (rounds != 1) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      share(p, total, cta);
+      if (left > 0) it = find_unit<KT>(p, start, lane, at);
+      return;
+    }
+    int sum = x.T;  // at most 32 x 2^31 / KT: 32 bits do
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    share(p, __shfl_sync(0xffffffffu, sum, 31), cta);
+    if (left == 0) return;
+    const int src = __ffs(__ballot_sync(0xffffffffu, (int64_t)sum * p.c.Hkv > start)) - 1;
+    it.b = __shfl_sync(0xffffffffu, x.b, src);
+    it.tile = __shfl_sync(0xffffffffu, x.tile, src);
+    it.n = __shfl_sync(0xffffffffu, x.n, src);
+    it.first = __shfl_sync(0xffffffffu, x.first, src);
+    it.cu = __shfl_sync(0xffffffffu, x.cu, src);
+    it.kt.ns = __shfl_sync(0xffffffffu, x.kt.ns, src);
+    it.kt.total = __shfl_sync(0xffffffffu, x.kt.total, src);
+    it.kt.lo = __shfl_sync(0xffffffffu, x.kt.lo, src);
+    it.kt.cut = __shfl_sync(0xffffffffu, x.kt.cut, src);
+    it.T = __shfl_sync(0xffffffffu, x.T, src);
+    it.place(start - (int64_t)(__shfl_sync(0xffffffffu, sum, src) - it.T) * p.c.Hkv, at);
+  }
+
+ private:
+  __device__ __forceinline__ void share(const CacheAttnParams& p, int64_t tiles, int cta) {
+    W = tiles * p.c.Hkv;
+    ctas = ctas_used(W, p.ctas);
+    start = run_start(W, ctas, cta);
+    left = cta < ctas ? run_start(W, ctas, cta + 1) - start : 0;
+  }
+};
 
 // One warp per (packed token, head): joins the partials of the item that the
 // token's rows lie in, if there is more than one. rows: of a partial.

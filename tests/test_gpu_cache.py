@@ -228,6 +228,24 @@ def test_nothing_to_do(sparge):
     attn_check(sparge, "bf16", 2, 1, 64, 16, [5], [0], CAUSAL, extra=4)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("max_new", [1, 16, 200])
+@pytest.mark.parametrize("B", [1, 40])
+def test_all_sequences_without_new_tokens(sparge, kind, max_new, B):
+    """Whatever max_new promised: no row is written."""
+    attn_check(sparge, kind, 4, 2, 128, 16, [100] * B, [0] * B, CAUSAL, max_new=max_new, extra=6)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 70])
+def test_where_the_new_tokens_stand_in_a_batch(sparge, kind, new):
+    """The sequences with new tokens among the first 32, behind them, in both parts; more than 32 row tiles of one."""
+    for has in ((0, 31), (32,), (35, 37), (31, 32), (5, 39)):
+        attn_check(sparge, kind, 4, 2, 64, 16, [30 * (b % 7) for b in range(40)], [new if b in has else 0 for b in range(40)],
+                   CAUSAL, extra=2)
+    attn_check(sparge, kind, 4, 1, 64, 64, [10, 300], [1, 2200 if new > 1 else 1], (50, 0, 0, 1), max_new=new)
+
+
 def test_offsets_past_32_bits(sparge):
     """A pool of over 2^32 bytes and 2^31 values for each of K and V, its last pages in use."""
     Hkv, page, d = 8, 128, 128
