@@ -289,14 +289,18 @@ struct CacheRun {
   }
 };
 
-// One warp per (packed token, head): joins the partials of the item that the
-// token's rows lie in, if there is more than one. rows: of a partial.
-template <int D>
+// L lanes per (packed token, head): joins the partials of the item that the
+// token's rows lie in, if there is more than one. rows: of a partial. A row is
+// a chain of four loads (length, owner, sums, partials), so with many rows a
+// warp takes four of them at once (a call over five chunks 130 -> 123 us); with
+// few, whole warps share out the many partials that a row then has.
+template <int D, int L>
 __global__ void __launch_bounds__(128) cache_combine_kernel(const CacheAttnParams p, int rows) {
   grid_wait();
-  constexpr int C = D / 32;  // neighbouring channels per lane
-  const int lane = threadIdx.x % 32;
-  const int64_t id = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+  constexpr int C = D / L, V = C < 4 ? C : 4, N = C / V;  // channels per lane, N runs of V neighbours
+  const int lane = threadIdx.x % 32, sub = lane % L;
+  const unsigned group = L == 32 ? 0xffffffffu : ((1u << (L % 32)) - 1u) << (lane - sub);
+  const int64_t id = (int64_t)blockIdx.x * (128 / L) + threadIdx.x / L;
   const int t = (int)(id / p.H), h = (int)(id % p.H);
   if (t >= min(__ldg(p.c.cu + p.c.B), p.c.tokens)) return;
   const int4 own = p.owners[(int64_t)t * p.c.Hkv + h / p.G];
@@ -305,36 +309,45 @@ __global__ void __launch_bounds__(128) cache_combine_kernel(const CacheAttnParam
   if (c0 < 0 || c0 > c1 || c1 >= p.ctas || r < 0 || r >= rows) return;  // never noted: the kernel before gave up a wait
   auto slot = [&](int c) { return (int64_t)(2 * c + (c == c0 ? own.y : 0)) * rows + r; };
   float m = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[slot(c)].x);
+  for (int c = c0 + sub; c <= c1; c += L) m = fmaxf(m, p.part_ml[slot(c)].x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float l = 0.0f, o[C] = {};
-  for (int b = c0; b <= c1; b += 32) {
-    const int n = min(32, c1 + 1 - b);
-    const float2 ml = lane < n ? p.part_ml[slot(b + lane)] : make_float2(0.0f, 0.0f);
+  for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(group, m, o));
+  float l = 0.0f, o[N][V] = {};
+  for (int b = c0; b <= c1; b += L) {
+    const int n = min(L, c1 + 1 - b);
+    const float2 ml = sub < n ? p.part_ml[slot(b + sub)] : make_float2(0.0f, 0.0f);
     const float f = ml.y == 0.0f ? 0.0f : exp2f(ml.x - m);  // 0: saw nothing
     l += ml.y * f;
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
-      const float fi = __shfl_sync(0xffffffffu, f, i);
-      const float* src = p.part_o + slot(b + i) * D + lane * C;
-      float v[C];
-      if (C == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
-      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+      const float fi = __shfl_sync(group, f, i, L);
+      const float* src = p.part_o + slot(b + i) * D + sub * V;
+      float v[N][V];
 #pragma unroll
-      for (int k = 0; k < C; ++k) o[k] += v[k] * fi;
+      for (int j = 0; j < N; ++j) {
+        if (V == 4) *reinterpret_cast<float4*>(v[j]) = *reinterpret_cast<const float4*>(src + j * L * V);
+        else *reinterpret_cast<float2*>(v[j]) = *reinterpret_cast<const float2*>(src + j * L * V);
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int k = 0; k < V; ++k) o[j][k] += v[j][k] * fi;
     }
   }
-  l = warp_sum(l);
+#pragma unroll
+  for (int x = L / 2; x > 0; x >>= 1) l += __shfl_xor_sync(group, l, x);
   const int64_t row = (int64_t)t * p.H + h;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint32_t w[C / 2];
 #pragma unroll
-  for (int k = 0; k < C / 2; ++k) w[k] = pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
-  __nv_bfloat16* out = p.O + row * D + lane * C;
-  if (C == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[C / 2 - 1]);
-  else *reinterpret_cast<uint32_t*>(out) = w[0];
-  if (p.lse && lane == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  for (int j = 0; j < N; ++j) {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) w[k] = pack_bf16x2(o[j][2 * k] * inv, o[j][2 * k + 1] * inv);
+    __nv_bfloat16* out = p.O + row * D + (j * L + sub) * V;
+    if (V == 4) *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[V / 2 - 1]);
+    else *reinterpret_cast<uint32_t*>(out) = w[0];
+  }
+  if (p.lse && sub == 0) p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace sparge

@@ -281,16 +281,24 @@ cudaError_t launch_decode(const CUtensorMap& mk, const CUtensorMap& mv, const Ca
   return cudaGetLastError();
 }
 
+// Whole warps where the rows fit on the SMs at once that way (64 warps each), else eight lanes a row.
+template <int D>
+cudaError_t launch_combine(const CacheAttnParams& p, int rows, cudaStream_t st) {
+  const int64_t n = (int64_t)p.c.tokens * p.H;
+  if (n <= 64 * (int64_t)sm_count())
+    return launch_next(cache_combine_kernel<D, 32>, (unsigned)ceil_div(n, 4), 128, 0, st, p, rows);
+  return launch_next(cache_combine_kernel<D, 8>, (unsigned)ceil_div(n, 16), 128, 0, st, p, rows);
+}
+
 template <int D, bool E4M3>
 sparge_status launch_cache_attn(const sparge_cache* c, const CacheAttnParams& p, const AttnPlan& plan, cudaStream_t st) {
   CUtensorMap mk, mv;
   if (!make_map_pages(&mk, c->k, c) || !make_map_pages(&mv, c->v, c)) return SPARGE_ERR_CUDA;
-  const unsigned join = (unsigned)ceil_div((int64_t)p.c.tokens * p.H, 4);
   cudaError_t e;
   if (plan.rows <= 16) {
     e = plan.rows == 8 ? launch_decode<D, E4M3, 1>(mk, mv, p, st) : launch_decode<D, E4M3, 2>(mk, mv, p, st);
     if (e != cudaSuccess) return cuda_status(e);
-    return cuda_status(launch_next(cache_combine_kernel<D>, join, 128, 0, st, p, plan.rows));
+    return cuda_status(launch_combine<D>(p, plan.rows, st));
   }
   CUtensorMap mq;
   if (!make_map_q(&mq, p, D, plan.tpt / 2)) return SPARGE_ERR_CUDA;
@@ -299,7 +307,7 @@ sparge_status launch_cache_attn(const sparge_cache* c, const CacheAttnParams& p,
   cache_chunk_kernel<D, E4M3><<<p.ctas, chunk_threads<E4M3>(), ChunkSmem<D, E4M3>::kBytes, st>>>(mq, mk, mv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_status(e);
-  return cuda_status(launch_next(cache_combine_kernel<D>, join, 128, 0, st, p, plan.rows));
+  return cuda_status(launch_combine<D>(p, plan.rows, st));
 }
 
 }  // namespace
