@@ -382,8 +382,12 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
     constexpr int CH = D / 16;             // 16-code pieces per row
     constexpr int N = kWTile * CH / 128;   // pieces per thread and tile
     constexpr int U = 4;                   // at a time
-    const int tid = threadIdx.x - 384, c = tid % CH, r0 = tid / CH;
     constexpr int RS = 128 / CH;           // rows between a thread's pieces
+    // Eight neighbouring threads take four pieces of an even row and, of the odd row after it, the four of D = 64 or
+    // the other four of D = 128: their 16-byte reads and writes then lie in different banks (a row of eight pieces
+    // would write each bank twice).
+    const int tid = threadIdx.x - 384, odd = tid / 4 % 2;
+    const int c = tid % 4 + (CH == 8 ? 4 * (tid / 8 % 2 ^ odd) : 0), r0 = tid / (2 * CH) * 2 + odd;
     uint32_t n = 0;
     bool ok = true;
     if (work) do {
