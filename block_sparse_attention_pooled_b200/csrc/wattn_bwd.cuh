@@ -186,10 +186,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
   // D_i comes from the forward's O, whose rounding to bf16 moves it by up to
   // 2^-8 |dO_i| |O_i|: harmless where O_i is a mean of many values, but of the
   // size of dS where a row sees few keys. So with few key tiles they are gone
-  // through twice, first for D_i = sum_j P_ij dP_ij in fp32. (With more than three
-  // tiles a row sees 256 keys or so.) 8 x 4000 rows, relative error of dQ: 2 keys
-  // 4.1e-3 -> 2.4e-3, 16 keys 2.8e-3 -> 2.4e-3, for 2 of 55 us a step.
-  const bool twice = T <= 3;
+  // through twice, first for D_i = sum_j P_ij dP_ij in fp32. Relative error of dQ
+  // over 8 x 4000 rows (the roundings of dS and dQ alone: 2.35e-3): 2 keys 4.1e-3
+  // -> 2.4e-3, 512 keys 2.53e-3 -> 2.44e-3, for 2 of 55 and 8 of 80 us a step;
+  // from nine tiles on it is below 2.5e-3 without.
+  const bool twice = T <= 8;
   const int U = twice ? 2 * T : T;
   auto key_of = [&](int u) { return kt.key0(u < T ? u : u - T); };
 
