@@ -56,33 +56,37 @@ void* want(const Tensor& t, const char* name, at::ScalarType dtype, at::IntArray
   return t.data_ptr();
 }
 
-// The stream to launch on, with the tensors' device current. Memory taken here
-// for a stream that is not the current one is not handed out again before that
-// stream is done with it.
+// The stream to launch on, with the tensors' device current. Memory is taken
+// from that stream's pool: what the current stream has freed may still be
+// written by work that is queued there. An output made for a stream that is
+// not the current one is also kept until the current one, where the caller
+// goes on, is done with it.
 class Launch {
  public:
   Launch(const at::Device& device, const StreamArg& stream) : device_(device) {
     if (c10::cuda::current_device() != device.index()) guard_.emplace(device);
-    auto current = c10::cuda::getCurrentCUDAStream(device.index());
-    handle_ = current.stream();
+    current_ = c10::cuda::getCurrentCUDAStream(device.index());
+    handle_ = current_->stream();
     if (stream) {
       if (stream->first != device.index()) refuse("the stream belongs to another device than the tensors");
       auto h = reinterpret_cast<cudaStream_t>(stream->second);
       if (h != handle_) {
         handle_ = h;
-        foreign_ = c10::cuda::getStreamFromExternal(h, device.index());
+        foreign_.emplace(c10::cuda::getStreamFromExternal(h, device.index()));
       }
     }
   }
   void* stream() const { return handle_; }
   Tensor make(at::IntArrayRef shape, at::ScalarType dtype) {
-    Tensor t = at::empty(shape, at::TensorOptions().dtype(dtype).device(device_));
-    if (foreign_) t.record_stream(*foreign_);
-    return t;
+    return at::empty(shape, at::TensorOptions().dtype(dtype).device(device_));
   }
   // The caller's tensor, or one made here.
   Tensor out(const MaybeTensor& t, const char* name, at::ScalarType dtype, at::IntArrayRef shape) {
-    if (!t) return make(shape, dtype);
+    if (!t) {
+      Tensor made = make(shape, dtype);
+      if (foreign_) made.record_stream(*current_);
+      return made;
+    }
     want(*t, name, dtype, shape, device_);
     return *t;
   }
@@ -102,8 +106,9 @@ class Launch {
  private:
   at::Device device_;
   cudaStream_t handle_;
-  std::optional<c10::cuda::CUDAStream> foreign_;
+  std::optional<c10::cuda::CUDAStream> current_;
   std::optional<c10::cuda::CUDAGuard> guard_;
+  std::optional<c10::cuda::CUDAStreamGuard> foreign_;
 };
 
 // ---------------------------------------------------------------- whole sequences

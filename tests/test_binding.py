@@ -164,3 +164,26 @@ def test_threads_call_at_once(lib):
         t.join()
     for i in range(4):
         assert len(got[i]) == 50 and all(torch.equal(o, want[i]) for o in got[i])
+
+
+@pytest.mark.gpu
+def test_outputs_for_another_stream(lib):
+    """Memory that the current stream has freed, with work on it still queued there, does not become another stream's
+    output; and an output is not handed out again while the current stream still reads it."""
+    ins = window_inputs(B=1, H=8, Hkv=2, N=1000)
+    want = lib.sparge_window_fwd(*ins, 20, 0)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(40_000_000)  # some 20 ms
+    torch.empty_like(want).fill_(7)
+    got = lib.sparge_window_fwd(*ins, 20, 0, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda._sleep(40_000_000)
+    copy = got.clone()
+    del got
+    with torch.cuda.stream(s):
+        torch.empty_like(want).fill_(9)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
