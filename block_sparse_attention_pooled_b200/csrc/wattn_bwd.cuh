@@ -328,11 +328,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
     }
     auto all_rows = [] { asm volatile("bar.sync 2, 256;" ::: "memory"); };
-    // The sum of both groups' shares of a row.
+    // The sum of both groups' shares of a row. The second barrier keeps the next
+    // call's shares out until all rows have read these: with one key tile no
+    // other wait lies between two calls.
     auto both = [&](float v) {
       dots[128 * wg + r] = v;
       all_rows();
-      return dots[r] + dots[128 + r];
+      const float sum = dots[r] + dots[128 + r];
+      all_rows();
+      return sum;
     };
     all_rows();
     float D_i = twice ? 0.0f : dots[r], more_D = 0.0f;

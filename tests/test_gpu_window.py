@@ -260,3 +260,22 @@ def test_gradients_of_rows_that_see_few_keys(sparge, win):
         assert (G[0][0, h].double() - dq).norm() <= 2.0 ** -8 * dq.norm()
         dK[h // 2] += dk
     assert (G[1][0].double() - dK).norm() <= 2.0 ** -8 * dK.norm()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,unit,right", [(128, 1, 0), (77, 1, 0), (128 * 12, 128, 0), (100, 1, -1)])
+def test_backward_of_single_key_tiles_repeats_itself(sparge, N, unit, right, d):
+    """Row tiles with one key tile sum each row over both halves of its columns twice, with nothing but the row sums'
+    own barriers in between: every one of many calls gives the same bits, which are the definition's gradients."""
+    Q, K, V, dO = inputs(2, 40, 20, N, d, seed=15)
+    win = (0 if unit > 1 else -1, right, 0, unit)
+    O, lse, want = check(sparge, *(t[:1, :2 if t.shape[1] == 40 else 1].contiguous() for t in (Q, K, V, dO)), win)
+    lse = torch.empty(2, 40, N, device="cuda")
+    O = sparge.sparge_window_fwd(Q, K, V, *win[:2], unit=unit, lse=lse)
+    runs = [sparge.sparge_window_bwd(Q, K, V, O, lse, dO, *win[:2], unit=unit) for _ in range(100)]
+    torch.cuda.synchronize()
+    assert sparge.device_status() == 0
+    assert torch.equal(runs[0][0][:1, :2], want[0])
+    for other in runs[1:]:
+        for a, b in zip(runs[0], other):
+            assert torch.equal(a, b)
