@@ -17,9 +17,11 @@
 // outside: a row of Q enters times the power of two that puts its largest
 // element at 2^14 (exact but below 2^-39 of that), a key's power joins its
 // score, and a value's power joins the exponent of its probability: with
-// x_j the score in log2 units and e_j the power of v_j, the running maximum is
-// that of x_j + e_j, P_j = 2^(x_j + e_j - M) <= 1, and the row sum takes
-// P_j 2^-e_j.
+// x_j the score in log2 units and e_j the power of v_j, the product takes
+// P_j = 2^(x_j + e_j - M), M the running maximum of x_j + e_j. The row sum is
+// kept apart, sum 2^(x_j - X) with X the running maximum of x_j: powers lie up
+// to 240 apart (a row of zeros has the least), so neither sum can be had from
+// the other's terms. The product is moved to the reference X when a warp is done.
 #pragma once
 #include <cuda.h>
 #include <cstdint>
@@ -282,6 +284,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
     // The lane's rows in the accumulators: 8 x + 2 c + y.
     int lo[R8][2], hi[R8][2];
     float m_run[R8][2], l_run[R8][2], o[D / 16][R8][4];
+    float x_run[R8][2];  // e4m3: the reference of l_run, over the lane's own keys
 #pragma unroll
     for (int x = 0; x < R8; ++x)
 #pragma unroll
@@ -289,7 +292,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
         const int i = it.first + t0 + min((8 * x + 2 * c + y) / p.G, tokens - 1);
         lo[x][y] = p.w.lo(i);
         hi[x][y] = p.w.hi(i, len);
-        m_run[x][y] = -INFINITY;
+        m_run[x][y] = x_run[x][y] = -INFINITY;
         l_run[x][y] = 0.0f;
       }
 #pragma unroll
@@ -363,25 +366,24 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
         }
       }
       // To log2 units; keys that a row does not see to -inf.
-      float unv[MT][2];  // e4m3: 2^-e_j of the lane's keys
+      float ev[MT][2];  // e4m3: the powers of the lane's keys' values
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          float pk = 1.0f, ev = 0.0f;
+          float pk = 1.0f;
           if (E4M3) {
             const int r = 16 * (k16 + mt) + g + 8 * z;
             pk = exp_scale((uint8_t)lds_u8(ex + r));
             const uint32_t b = lds_u8(ex + KT + r);
-            ev = b == 255 ? __int_as_float(0x7FC00000) : (float)((int)b - 127);
-            unv[mt][z] = __uint_as_float((254u - b) << 23);
+            ev[mt][z] = b == 255 ? __int_as_float(0x7FC00000) : (float)((int)b - 127);
           }
 #pragma unroll
           for (int x = 0; x < R8; ++x)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               float& v = s[mt][x][2 * z + y];
-              v = E4M3 ? fmaf(v * unq[x][y], pk, ev) : v * p.scale_log2;
+              v = E4M3 ? v * unq[x][y] * pk : v * p.scale_log2;
             }
         }
       if (!whole) {
@@ -408,9 +410,27 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
         float top[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          float m = fmaxf(s[0][x][y], s[0][x][2 + y]);
+          float m;
+          if (E4M3) {
+            float mx = fmaxf(s[0][x][y], s[0][x][2 + y]);
+            m = fmaxf(s[0][x][y] + ev[0][0], s[0][x][2 + y] + ev[0][1]);
 #pragma unroll
-          for (int mt = 1; mt < MT; ++mt) m = fmax3(m, s[mt][x][y], s[mt][x][2 + y]);
+            for (int mt = 1; mt < MT; ++mt) {
+              mx = fmax3(mx, s[mt][x][y], s[mt][x][2 + y]);
+              m = fmax3(m, s[mt][x][y] + ev[mt][0], s[mt][x][2 + y] + ev[mt][1]);
+            }
+            mx = fmaxf(mx, x_run[x][y]);
+            if (mx > x_run[x][y]) l_run[x][y] *= ex2_approx(x_run[x][y] - mx);
+            x_run[x][y] = mx;
+            const float ref = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              l_run[x][y] += ex2_approx(s[mt][x][y] - ref) + ex2_approx(s[mt][x][2 + y] - ref);
+          } else {
+            m = fmaxf(s[0][x][y], s[0][x][2 + y]);
+#pragma unroll
+            for (int mt = 1; mt < MT; ++mt) m = fmax3(m, s[mt][x][y], s[mt][x][2 + y]);
+          }
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
           top[y] = fmaxf(m, m_run[x][y]);
@@ -419,7 +439,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const float f = top[y] == -INFINITY ? 1.0f : ex2_approx(m_run[x][y] - top[y]);
-            l_run[x][y] *= f;
+            if (!E4M3) l_run[x][y] *= f;
             m_run[x][y] = top[y];
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
@@ -435,9 +455,14 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
-              const float e = ex2_approx(s[mt][x][2 * z + y] - ref);
-              l_run[x][y] += E4M3 && e > 0.0f ? e * unv[mt][z] : e;  // a masked key's power may be anything
-              s[mt][x][2 * z + y] = e;
+              float& v = s[mt][x][2 * z + y];
+              if (E4M3) {
+                const float e = ex2_approx(v - ref + ev[mt][z]);
+                v = whole || v != -INFINITY ? e : 0.0f;  // a masked key's power may be anything
+              } else {
+                v = ex2_approx(v - ref);
+                l_run[x][y] += v;
+              }
             }
         }
 #pragma unroll
@@ -496,16 +521,25 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
     for (int x = 0; x < R8; ++x)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
+        float ref = m_run[x][y], f = 1.0f;
+        if (E4M3) {
+          ref = x_run[x][y];
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, d));
+          if (x_run[x][y] != -INFINITY) l_run[x][y] *= ex2_approx(x_run[x][y] - ref);
+          // From M to X in two halves: the whole may lie below 2^-126.
+          if (m_run[x][y] != -INFINITY && ref != -INFINITY) f = ex2_approx(0.5f * (m_run[x][y] - ref));
+        }
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l_run[x][y] += __shfl_xor_sync(0xffffffffu, l_run[x][y], d);
         const int r = 8 * x + 2 * c + y;
-        if (g == 0) wml[warp * L::kRows + r] = make_float2(m_run[x][y], l_run[x][y]);
+        if (g == 0) wml[warp * L::kRows + r] = make_float2(ref, l_run[x][y]);
         float* dst = wo + (warp * L::kRows + r) * L::kOStride;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const int ch = E4M3 ? (D / 8) * g + 2 * k : 16 * k + g, ch2 = E4M3 ? ch + 1 : ch + 8;
-          dst[ch] = o[k][x][y];
-          dst[ch2] = o[k][x][2 + y];
+          dst[ch] = E4M3 ? o[k][x][y] * f * f : o[k][x][y];
+          dst[ch2] = E4M3 ? o[k][x][2 + y] * f * f : o[k][x][2 + y];
         }
       }
     asm volatile("bar.sync 1, %0;" ::"n"(NW * 32) : "memory");

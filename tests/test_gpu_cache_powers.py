@@ -1,0 +1,120 @@
+"""Attention over an e4m3 cache whose rows have powers far apart, against the 64-bit definition: through the kernel for
+up to 16 rows a sequence (4 heads, 1 and 4 new tokens) and the one for more (20 new tokens)."""
+import math
+
+import pytest
+import torch
+
+from window_ref import close, e4m3_rows, rows_fwd, visible
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sparge():
+    from block_sparse_attention_pooled_b200 import build
+
+    build.build()
+    from block_sparse_attention_pooled_b200 import sparge as m
+
+    return m
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def normal(seed, *shape):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda")
+
+
+def cache_of(sparge, k, v, page=64):
+    """k, v [n, d] as the cache of one sequence with one K/V head."""
+    n, d = k.shape
+    pages = -(-n // page)
+    kp, vp = (torch.full((pages, 1, page, d), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+    exp = {x: torch.full((pages, 1, page), 255, dtype=torch.uint8, device="cuda") for x in ("k_exp", "v_exp")}
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").flip(0)[None].contiguous()
+    bf = [x.to(torch.bfloat16)[:, None].contiguous() for x in (k, v)]
+    sparge.sparge_cache_write(*bf, kp, vp, table, ints(0), ints(0, n), **exp)
+    return (kp, vp, table), exp, [e4m3_rows(x)[0][:, 0] for x in bf]
+
+
+def attend(sparge, Q, cache, exp, n, win=(-1, 0, 0, 1)):
+    new, lse = Q.shape[0], torch.empty(Q.shape[:2], device="cuda")
+    O = sparge.sparge_cache_attn(Q, *cache, ints(n - new), ints(0, new), new, n, *win[:2], sinks=win[2], unit=win[3],
+                                 lse=lse, **exp)
+    torch.cuda.synchronize()
+    assert sparge.device_status() == 0
+    return O, lse
+
+
+def compare(O, lse, Q, k64, v64, win=(-1, 0, 0, 1), floor=None):
+    """floor: [rows, d] for each head, what a probability's rounding may add (none where probabilities are bf16)."""
+    n, new = k64.shape[0], Q.shape[0]
+    at = torch.arange(n, device="cuda")
+    seen = visible(at[-new:], at, n, *win)
+    for h in range(Q.shape[1]):
+        o, ls, to, P, tl = rows_fwd(Q[:, h], k64, v64, seen)
+        close(lse[:, h], ls, tl, f"lse, head {h}")
+        close(O[:, h], o, to if floor is None else to + floor(P), f"O, head {h}")
+
+
+def check(sparge, k, v, Q, win=(-1, 0, 0, 1), page=64):
+    cache, exp, (k64, v64) = cache_of(sparge, k, v, page)
+    O, lse = attend(sparge, Q, cache, exp, k.shape[0], win)
+    compare(O, lse, Q, k64, v64, win)
+    return O, lse
+
+
+def one_against_many(many, below, d, new, seed):
+    """The first key scores 0 and the others `below` (log2) less, for 4 heads; the last `new` tokens are among them."""
+    k = torch.zeros(many + 1, d, device="cuda")
+    k[1:, 0] = -8.0
+    Q = torch.zeros(new, 4, d, device="cuda")
+    Q[..., 0] = below / 8.0 * math.sqrt(d) / math.log2(math.e)
+    return k, Q.to(torch.bfloat16), normal(seed, many + 1, d)
+
+
+NEW = pytest.mark.parametrize("new", [1, 4, 20])
+
+
+@NEW
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("top,many,below", [(100.0, 4096, 12), (3.0, 4096, 17), (2.0 ** 20, 40, 0), (2.0 ** 90, 40, 0)])
+def test_keys_whose_value_is_zero_count(sparge, top, many, below, d, new):
+    """One key with a value of `top` among many whose value is 0: they only dilute it."""
+    k, Q, v = one_against_many(many, below, d, new, 1)
+    v = v.clamp(-1, 1) * top
+    v[1:] = 0
+    check(sparge, k, v, Q)
+
+
+@NEW
+@pytest.mark.parametrize("zeros", [2048, 30000])
+def test_long_runs_of_zero_rows(sparge, zeros, new):
+    """Keys and values of 0 (a stretch that was never written but is seen), then ordinary rows; then nothing else."""
+    n = zeros + 5000
+    k, v = normal(2, n, 128), normal(3, n, 128)
+    k[:zeros] = 0
+    v[:zeros] = 0
+    Q = normal(4, new, 4, 128).to(torch.bfloat16)
+    check(sparge, k, v, Q)
+    O, _ = check(sparge, k[:zeros].contiguous(), v[:zeros].contiguous(), Q)
+    assert not O.any()
+
+
+@NEW
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("win", [(-1, 0, 0, 1), (700, 0, 30, 1)])
+def test_rows_of_different_powers(sparge, win, d, new):
+    """Magnitudes of K and V that differ from row to row by up to 2^12, some rows 0, scores of some dozens."""
+    n = 1500
+    k, v = normal(5, n, d), normal(6, n, d)
+    k *= torch.exp2(normal(7, n, 1).clamp(-3, 3))
+    v *= torch.exp2(2 * normal(8, n, 1).clamp(-3, 3))
+    v[::7] = 0
+    k[::5] = 0
+    check(sparge, k, v, normal(9, new, 4, d).to(torch.bfloat16) * 2, win, page=16)
