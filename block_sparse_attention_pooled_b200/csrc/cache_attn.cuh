@@ -18,7 +18,10 @@
 // element at 2^14 (exact but below 2^-39 of that), a key's power joins its
 // score, and a value's power joins the exponent of its probability: with
 // x_j the score in log2 units and e_j the power of v_j, the product takes
-// P_j = 2^(x_j + e_j - M), M the running maximum of x_j + e_j. The row sum is
+// P_j = 2^(x_j + e_j - M + 15), M the running maximum of x_j + e_j: at the top
+// of fp16's range, so that what lies down to 2^-29 of the largest keeps 11 bits
+// and half a step below that is 2^-40 of it. (Half a step of the largest key's
+// own codes is 2^-10 of its power.) The row sum is
 // kept apart, sum 2^(x_j - X) with X the running maximum of x_j: powers lie up
 // to 240 apart (a row of zeros has the least), so neither sum can be had from
 // the other's terms. The product is moved to the reference X when a warp is done.
@@ -138,6 +141,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
   using L = DecSmem<D, E4M3, R8>;
   constexpr int NS = L::NS, NW = L::NW, KT = L::KT, SPLIT = L::SPLIT;
   constexpr int MT = KT / 16 / SPLIT;  // a warp's 16-key steps of a tile
+  constexpr float kPTop = 15.0f;       // e4m3: the largest P is 2^15 (fp16 ends at 2^16)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
             for (int z = 0; z < 2; ++z) {
               float& v = s[mt][x][2 * z + y];
               if (E4M3) {
-                const float e = ex2_approx(v - ref + ev[mt][z]);
+                const float e = ex2_approx(v - ref + (ev[mt][z] + kPTop));
                 v = whole || v != -INFINITY ? e : 0.0f;  // a masked key's power may be anything
               } else {
                 v = ex2_approx(v - ref);
@@ -528,7 +532,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
           for (int d = 4; d < 32; d <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, d));
           if (x_run[x][y] != -INFINITY) l_run[x][y] *= ex2_approx(x_run[x][y] - ref);
           // From M to X in two halves: the whole may lie below 2^-126.
-          if (m_run[x][y] != -INFINITY && ref != -INFINITY) f = ex2_approx(0.5f * (m_run[x][y] - ref));
+          if (m_run[x][y] != -INFINITY && ref != -INFINITY) f = ex2_approx(0.5f * (m_run[x][y] - kPTop - ref));
         }
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l_run[x][y] += __shfl_xor_sync(0xffffffffu, l_run[x][y], d);

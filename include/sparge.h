@@ -398,7 +398,14 @@ sparge_status sparge_cache_read(const sparge_cache* cache, const sparge_cache_ba
  *   max_new, max_len  bounds of a sequence's new tokens and of L, >= 1. They
  *               choose how the work is split, not what is computed.
  *   O           bf16 [tokens, H, d], contiguous;  lse: optional float [tokens, H].
- * Precision as sparge_window_fwd; e4m3 rows enter the products as exact bf16.
+ * Precision: bf16 as sparge_window_fwd. e4m3: the codes enter the products
+ * exactly, the rows' powers join the fp32 scores and probabilities. With more
+ * than 16 rows (heads per K/V head times new tokens) a sequence, P is rounded
+ * to bf16. Up to 16, P times its value's power is rounded to fp16, with the
+ * largest of a row at 2^15: 11 bits down to 2^-29 of the largest, and half a
+ * step of 2^-40 of it below that (the largest row's own codes end at 2^-10 of
+ * its power); Q is exact down to 2^-31 of its row's largest element, and off by
+ * at most 2^-39 of it below.
  * A place of the cache that no position of the batch stands for may hold
  * anything, NaN too. Workspace: sparge_cache_attn_workspace_bytes(...), asked with
  * the tensors' device current (0 if nothing is to be done or an argument is invalid). */

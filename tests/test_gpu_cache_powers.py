@@ -118,3 +118,48 @@ def test_rows_of_different_powers(sparge, win, d, new):
     v[::7] = 0
     k[::5] = 0
     check(sparge, k, v, normal(9, new, 4, d).to(torch.bfloat16) * 2, win, page=16)
+
+
+def fp16_floor(code, power):
+    """What probabilities in fp16 may add. A P_j 2^e_j enters as a multiple of its row's largest, W, which stands at
+    2^15: half a step of fp16 below 2^-14 is 2^-25, that is 2^-40 W, for each key's code."""
+    def floor(P):
+        W = (P * power[None]).amax(1)
+        return 2.0 ** -40 * W[:, None] * ((P > 0).double() @ code.abs())
+    return floor
+
+
+def check_with_floor(sparge, k, v, Q):
+    cache, exp, (k64, v64) = cache_of(sparge, k, v)
+    byte = e4m3_rows(v.to(torch.bfloat16))[1]
+    power = torch.exp2(byte.double() - 127)
+    O, lse = attend(sparge, Q, cache, exp, k.shape[0])
+    compare(O, lse, Q, k64, v64, floor=fp16_floor(v64 / power[:, None], power))
+
+
+@pytest.mark.parametrize("new", [1, 4])
+@pytest.mark.parametrize("below", [17.3, 21.7, 26])
+@pytest.mark.parametrize("many", [63, 6000])  # all with the best key in one warp's hands; most of them elsewhere
+@pytest.mark.parametrize("d", [64, 128])
+def test_channels_that_the_best_key_leaves_empty(sparge, d, many, below, new):
+    """The best key holds 0 in half of its channels: there O comes from the many keys `below` binades down, each
+    kept to fp16's 11 bits, as they are with more rows (bf16's 8 bits). The tolerance has no part for lost keys."""
+    k, Q, v = one_against_many(many, below, d, 20, 10)
+    v = v.abs().clamp(0.25, 3)
+    v[0, ::2] = 0
+    v[0, 1::2] = 3.0
+    few, _ = check(sparge, k, v, Q[-new:].contiguous())
+    many, _ = check(sparge, k, v, Q)
+    assert ((few.double() - many[-new:].double()).abs() <= 2.5 * 2.0 ** -8 * few.double().abs()).all()
+
+
+@pytest.mark.parametrize("new", [1, 4, 20])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_powers_dozens_apart(sparge, d, new):
+    """V's rows between 2^-40 and 2^40 (some rows 0), scores of some dozens, K's rows 2^6 apart."""
+    n = 1500
+    k, v = normal(11, n, d), normal(12, n, d)
+    k *= torch.exp2(normal(13, n, 1).clamp(-3, 3))
+    v *= torch.exp2(20 * normal(14, n, 1).clamp(-2, 2))
+    v[::9] = 0
+    check_with_floor(sparge, k, v, normal(15, new, 4, d).to(torch.bfloat16))
