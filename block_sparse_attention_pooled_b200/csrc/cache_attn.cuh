@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
           for (int d = 4; d < 32; d <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, d));
           if (x_run[x][y] != -INFINITY) l_run[x][y] *= ex2_approx(x_run[x][y] - ref);
           // From M to X in two halves: the whole may lie below 2^-126.
-          if (m_run[x][y] != -INFINITY && ref != -INFINITY) f = ex2_approx(0.5f * (m_run[x][y] - kPTop - ref));
+          if (m_run[x][y] != -INFINITY && ref != -INFINITY) f = ex2_approx(0.5f * (m_run[x][y] - ref - kPTop));
         }
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l_run[x][y] += __shfl_xor_sync(0xffffffffu, l_run[x][y], d);

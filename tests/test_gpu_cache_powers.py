@@ -163,3 +163,17 @@ def test_rows_of_powers_dozens_apart(sparge, d, new):
     v *= torch.exp2(20 * normal(14, n, 1).clamp(-2, 2))
     v[::9] = 0
     check_with_floor(sparge, k, v, normal(15, new, 4, d).to(torch.bfloat16))
+
+
+@NEW
+@pytest.mark.parametrize("power", [10, 20, 27])
+def test_equal_scores_however_large(sparge, power, new):
+    """Scores of 8 * 2^power for three keys (exact in 32 bits) and of the opposite sign for the others: O is the mean of
+    the three's values."""
+    n, d = 300, 64
+    k, v = torch.zeros(n, d, device="cuda"), normal(18, n, d)
+    k[:, 0] = -8.0
+    k[[3, 70, 200], 0] = 8.0
+    Q = torch.zeros(new, 4, d, device="cuda")
+    Q[..., 0] = 2.0 ** power
+    check(sparge, k, v, Q.to(torch.bfloat16))
