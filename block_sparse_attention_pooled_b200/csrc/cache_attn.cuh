@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
     left -= stop - at;
     // Q as operand B: rows 8 x + g, channels as the keys' operand has them.
     uint32_t q[R8][D / 16][2];
-    float unq[R8][2];  // e4m3: what undoes the scaling of the lane's accumulator rows
+    float unq[R8][2], unq2[R8][2];  // e4m3: two factors that undo the scaling of the lane's accumulator rows
 #pragma unroll
     for (int x = 0; x < R8; ++x) {
       const int r = 8 * x + g;
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
           for (int h = 0; h < 2; ++h) top = max(top, max(q[x][k][h] & 0x7FFFu, (q[x][k][h] >> 16) & 0x7FFFu));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int shift = min(14 - ((int)(top >> 7) - 127), 100);
+        const int shift = min(14 - ((int)(top >> 7) - 127), 127);
         const float f = __uint_as_float((uint32_t)(127 + shift) << 23);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
@@ -280,8 +280,11 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
             q[x][k][h] = pack_f16x2(__uint_as_float(q[x][k][h] << 16) * f, __uint_as_float(q[x][k][h] & 0xFFFF0000u) * f);
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const int sh = __shfl_sync(0xffffffffu, shift, 4 * (2 * c + y));
-          unq[x][y] = p.scale_log2 * __uint_as_float((uint32_t)(127 - sh) << 23);
+          // One before and one after the key's power: all of 2^-shift at once
+          // could leave the range where the score does not.
+          const int sh = __shfl_sync(0xffffffffu, shift, 4 * (2 * c + y)), half = sh / 2;
+          unq[x][y] = p.scale_log2 * __uint_as_float((uint32_t)(127 - half) << 23);
+          unq2[x][y] = __uint_as_float((uint32_t)(127 - (sh - half)) << 23);
         }
       }
     }
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               float& v = s[mt][x][2 * z + y];
-              v = E4M3 ? v * unq[x][y] * pk : v * p.scale_log2;
+              v = E4M3 ? v * unq[x][y] * pk * unq2[x][y] : v * p.scale_log2;
             }
         }
       if (!whole) {

@@ -177,3 +177,26 @@ def test_equal_scores_however_large(sparge, power, new):
     Q = torch.zeros(new, 4, d, device="cuda")
     Q[..., 0] = 2.0 ** power
     check(sparge, k, v, Q.to(torch.bfloat16))
+
+
+@NEW
+@pytest.mark.parametrize("power", [-124, -110, -90, 90, 110, 116])
+def test_queries_of_any_magnitude(sparge, power, new):
+    """Q around 2^power and K around 2^-power: scores as of ordinary ones, down to rows of Q that are almost subnormal."""
+    n, d = 300, 128
+    k, v = normal(19, n, d).clamp(-3, 3), normal(20, n, d)
+    Q = normal(21, new, 4, d)
+    Q = torch.where(Q.abs() < 0.25, 0.25, Q) * 2.0 ** power
+    check(sparge, k * 2.0 ** -power, v, Q.to(torch.bfloat16))
+
+
+@NEW
+def test_large_scores_of_large_queries(sparge, new):
+    """Scores of some 2^12 from a Q of 2^126 and keys near the least power: no product on the way overflows."""
+    n, d = 300, 64
+    k, v = torch.zeros(n, d, device="cuda"), normal(22, n, d)
+    k[:, 0] = -(2.0 ** -111)
+    k[[3, 70, 200], 0] = 2.0 ** -111
+    Q = torch.zeros(new, 4, d, device="cuda")
+    Q[..., 0] = 2.0 ** 126
+    check(sparge, k, v, Q.to(torch.bfloat16))
