@@ -38,9 +38,9 @@ __device__ __forceinline__ int64_t cache_row(const CacheView& c, int b, int p) {
   return (((int64_t)id * c.Hkv) << c.page_shift) + (p & ((1 << c.page_shift) - 1));
 }
 
-// 2^(byte - 127), NaN for byte 255 (bytes 10 .. 246 are written).
+// 2^(byte - 127), NaN for byte 255 (bytes 10 .. 246 are written; 0 is subnormal).
 __device__ __forceinline__ float exp_scale(uint8_t byte) {
-  return byte == 255 ? __int_as_float(0x7FC00000) : __uint_as_float((uint32_t)byte << 23);
+  return byte == 255 ? __int_as_float(0x7FC00000) : __uint_as_float(max((uint32_t)byte << 23, 0x400000u));
 }
 
 // The power of a row whose largest magnitude is a (finite): the least with

@@ -318,7 +318,10 @@ size_t sparge_window_workspace_bytes(int op, const sparge_window_shape* shape, c
  *               matter. NULL: N for all.
  *   lse         optional output, float [B,H,N], natural logarithm.
  * Values at positions before L have to be finite: a key that one row of a
- * tile sees and another does not reaches the latter as 0 * v.
+ * tile sees and another does not reaches the latter as 0 * v. Scores and sums
+ * are in 32 bits: q . k / sqrt(d) has to stay below 2^29 in magnitude, and V's
+ * magnitude times the number of keys that a row sees below 2^119 (the sum is
+ * divided at the end).
  * Limits: d 64 or 128, B * Hkv <= 65535. Workspace:
  * sparge_window_workspace_bytes(SPARGE_OP_WINDOW_FWD, ...). */
 sparge_status sparge_window_fwd(const void* Q, const void* K, const void* V, const sparge_window_shape* shape,
@@ -347,7 +350,9 @@ sparge_status sparge_window_bwd(const void* Q, const void* K, const void* V, con
  *   k, v        [pages, Hkv, page, d]: bf16, or e4m3 codes.
  *   k_exp, v_exp  e4m3 only: uint8 [pages, Hkv, page], the power of two of each
  *               (token, head) row: value = code * 2^(byte - 127). Byte 255: the
- *               row is NaN as a whole.
+ *               row is NaN as a whole. sparge_cache_write stores finite codes
+ *               and bytes 10 .. 246, whose values are all exact in bf16; with
+ *               the other bytes a value has to be finite and exact in bf16 too.
  * A page id outside [0, pages), or a position past max_pages * page, is a place
  * that does not exist: it is not written, reads back as 0, and no row sees it
  * (a rolling cache drops a page by writing -1 into the table). */
@@ -398,7 +403,8 @@ sparge_status sparge_cache_read(const sparge_cache* cache, const sparge_cache_ba
  *   max_new, max_len  bounds of a sequence's new tokens and of L, >= 1. They
  *               choose how the work is split, not what is computed.
  *   O           bf16 [tokens, H, d], contiguous;  lse: optional float [tokens, H].
- * Precision: bf16 as sparge_window_fwd. e4m3: the codes enter the products
+ * Precision, and the magnitudes of scores and V that 32 bits hold: bf16 as
+ * sparge_window_fwd. e4m3: the same magnitudes; the codes enter the products
  * exactly, the rows' powers join the fp32 scores and probabilities. With more
  * than 16 rows (heads per K/V head times new tokens) a sequence, P is rounded
  * to bf16. Up to 16, P times its value's power is rounded to fp16, with the

@@ -200,3 +200,33 @@ def test_large_scores_of_large_queries(sparge, new):
     Q = torch.zeros(new, 4, d, device="cuda")
     Q[..., 0] = 2.0 ** 126
     check(sparge, k, v, Q.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("new", [1, 4, 20])
+@pytest.mark.parametrize("byte", [0, 1, 9, 247, 254])
+def test_bytes_that_the_writer_does_not_store(sparge, byte, new):
+    """Every byte but 255 is the power byte - 127, in reading and in attention, as far as bf16 holds the values: in K
+    (with a Q of the opposite magnitude) and in V, where the sums before the division by the row's have to fit 32 bits
+    (150 keys of 2^120 do, of 2^127 do not)."""
+    n, d, page = 150, 64, 16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(16)
+    pages = -(-n // page)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None].contiguous()
+    # codes between 1/2 and 15/8: their values are exact in bf16 at every power, subnormal ones included
+    codes = [(torch.randint(0x30, 0x40, (pages, 1, page, d), generator=g, device="cuda", dtype=torch.uint8)
+              | torch.randint(0, 2, (pages, 1, page, d), generator=g, device="cuda", dtype=torch.uint8) << 7)
+             .view(torch.float8_e4m3fn) for _ in range(2)]
+    for which in (0, 1):
+        exp = [torch.full((pages, 1, page), b, dtype=torch.uint8, device="cuda") for b in ((byte, 127) if which == 0 else (127, byte))]
+        kv = [(c.float().double() * torch.exp2(e.double() - 127)[..., None]).transpose(1, 2).flatten(0, 1)[:n, 0]
+              for c, e in zip(codes, exp)]
+        both = {"k_exp": exp[0], "v_exp": exp[1]}
+        got = sparge.sparge_cache_read(*codes, table, ints(0), ints(0, n), n, **both)
+        for x, want in zip(got, kv):
+            assert torch.equal(x[:, 0].double(), want)
+        if byte == 254 and which == 1:
+            continue
+        Q = (normal(17, new, 4, d) * 2.0 ** (max(-120, min(120, 127 - byte)) if which == 0 else 0)).to(torch.bfloat16)
+        O, lse = attend(sparge, Q, (*codes, table), both, n)
+        compare(O, lse, Q, *kv)
