@@ -9,7 +9,11 @@
 // K and V come by TMA, one box per page, from a warp each (a box costs its
 // issuing lane some hundred cycles). bf16: straight into the ring. e4m3:
 // the codes into a slot of their own, from where four more warps write them
-// into the ring as bf16, each times its row's power: exact.
+// into the ring as bf16, each times its row's power: exact. A row of V that is
+// NaN goes there as zeros, or rows of the tile that do not see it would get
+// 0 * NaN, and sets a flag; the softmax warps that find it set at the end of an
+// item look for such rows among the keys of each of their rows. (Looking at the
+// powers of every tile took 171 -> 179 us for five chunks of 700 tokens.)
 #pragma once
 #include <cuda.h>
 #include <cstdint>
@@ -35,6 +39,30 @@ __device__ __forceinline__ void wait_quietly(uint32_t bar, uint32_t parity) {
   const unsigned long long t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < 1000000ull) {
   }
+}
+
+// Whether a row that sees [lo, hi) and the sinks of an item's key tiles t0 .. t1 - 1
+// sees a row of V that is NaN. Called by a whole warp, each lane with its row.
+__device__ __noinline__ bool sees_nan_value(const CacheAttnParams& p, KeyTiles kt, int b, int hk, int len, int t0, int t1,
+                                            int lo, int hi) {
+  const int lane = threadIdx.x % 32;
+  bool sees = false;
+  for (int t = t0; t < t1; ++t) {
+    const bool sink = t < kt.ns;
+    const int key0 = kt.key0(t), most = sink ? min(hi, kt.cut) : hi, mine = key0 + 4 * lane;
+    const int64_t row = mine < len ? cache_row(p.c, b, mine) : -1;  // of four keys: they lie in one page
+    uint32_t bytes = 0;
+    if (row >= 0) bytes = *reinterpret_cast<const uint32_t*>(p.c.v_exp + row + ((int64_t)hk << p.c.page_shift));
+    for (unsigned left = __ballot_sync(0xffffffffu, __vcmpeq4(bytes, 0xFFFFFFFFu) != 0); left; left &= left - 1) {
+      const int src = __ffs(left) - 1;
+      const uint32_t four = __shfl_sync(0xffffffffu, bytes, src);
+      for (int j = 0; j < 4; ++j) {
+        const int key = key0 + 4 * src + j;
+        sees |= (four >> (8 * j) & 0xFFu) == 0xFFu && key < most && (sink || key >= lo || key < p.w.sinks);
+      }
+    }
+  }
+  return sees;
 }
 
 template <bool E4M3>
@@ -63,7 +91,7 @@ struct ChunkSmem {
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
     cache_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const CacheAttnParams p) {
+                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CacheAttnParams p) {
   using L = ChunkSmem<D, E4M3>;
   constexpr int NS = L::NS, KT = kWTile;
   extern __shared__ uint8_t smem_raw[];
@@ -76,6 +104,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sgen + L::kOffTmem + 4);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile uint32_t* code_mask = reinterpret_cast<volatile uint32_t*>(sgen + L::kOffMask);  // boxes that exist
+  volatile uint32_t* nan_flag = code_mask + 2;  // e4m3: some row of V so far is NaN
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kNumBars; ++i) {
@@ -84,6 +113,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
       mbar_init(bar(i), rows || conv ? 128 : 1);
     }
     *abort_flag = 0;
+    *nan_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -360,16 +390,21 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
       ++nq;
       const int64_t row = (int64_t)(it.cu + tok) * p.H + it.hk * p.G + r % p.G;
       const bool none = l_run == 0.0f;
+      // What O is multiplied by: NaN if the row sees a row of V that is NaN. All
+      // of the item's V tiles are in O, so the flag is there.
+      float one = 1.0f;
+      if (E4M3 && __any_sync(0xffffffffu, *nan_flag != 0) && sees_nan_value(p, it.kt, it.b, it.hk, len, at0, stop, lo, hi))
+        one = __int_as_float(0x7FC00000);
       if (at0 == 0 && live && r % p.G == 0)
         p.owners[(int64_t)(it.cu + tok) * p.c.Hkv + it.hk] =
             make_int4(blockIdx.x, start < unit0, stop == it.T ? (int)blockIdx.x : run_owner(W, ctas, unit0 + it.T - 1),
                       x * tq * p.G + r);
       if (at0 == 0 && stop == it.T) {
-        store_row<D>(p.O + row * D, to, none ? 0.0f : 1.0f / l_run, none, live);
+        store_row<D>(p.O + row * D, to, none ? 0.0f : one / l_run, none, live);
         if (live && p.lse) p.lse[row] = none ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
       } else {
         const int64_t slot = (int64_t)(2 * blockIdx.x + (start < unit0 ? 1 : 0)) * (2 * kWTile) + (x * tq * p.G + r);
-        store_row_f32<D>(p.part_o + slot * D, to, 1.0f, false, live);
+        store_row_f32<D>(p.part_o + slot * D, to, one, false, live);
         if (live) p.part_ml[slot] = make_float2(m_run, l_run);
       }
       tc_fence_before();
@@ -404,6 +439,7 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
         if (!ok) break;
         const uint32_t dst = sKv + slot * L::kTileBytes;
         const uint32_t line0 = dst + (2 * c / 8) * (kWTile * 128);
+        const uint32_t nan_row = is_v ? 0u : 0x7FC0u;  // what such a row's codes are multiplied by
 #pragma unroll 1
         for (int k0 = 0; k0 < N; k0 += U) {
           uint4 code[U];
@@ -419,17 +455,19 @@ __global__ void __launch_bounds__(chunk_threads<E4M3>(), 1)
             const int r = r0 + (k0 + k) * RS;
             const bool here = key0 + r < len && (there >> (r >> box_shift) & 1u);
             // 2^(e + 120) as bf16, twice; 2^120 and 2^e in two steps where that is out of range. 0: does not exist
-            // (the codes there may be anything, but as bf16 they are finite).
+            // (the codes there may be anything, but as bf16 they are finite). A row that is NaN counts as far.
             const bool far = here && e[k] > 134;
-            const uint32_t p1 = !here ? 0u : (e[k] == 255 ? 0x7FC0u : (far ? 247u : e[k] + 120u) << 7) * 0x10001u;
+            const uint32_t p1 = !here ? 0u : (e[k] == 255 ? nan_row : (far ? 247u : e[k] + 120u) << 7) * 0x10001u;
             const uint32_t w[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
             uint32_t v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               v[j] = bf16x2_mul(codes_to_bf16(__byte_perm(w[j / 2], 0, j & 1 ? 0x4342 : 0x4140)), p1);
             if (far) {
+              if (e[k] == 255 && is_v) *nan_flag = 1;
+              const uint32_t p2 = (e[k] == 255 ? 0x3F80u : e[k] << 7) * 0x10001u;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] = bf16x2_mul(v[j], (e[k] << 7) * 0x10001u);
+              for (int j = 0; j < 8; ++j) v[j] = bf16x2_mul(v[j], p2);
             }
             const uint32_t line = line0 + r * 128;
 #pragma unroll

@@ -413,7 +413,10 @@ sparge_status sparge_cache_read(const sparge_cache* cache, const sparge_cache_ba
  * its power); Q is exact down to 2^-31 of its row's largest element, and off by
  * at most 2^-39 of it below.
  * A place of the cache that no position of the batch stands for may hold
- * anything, NaN too. Workspace: sparge_cache_attn_workspace_bytes(...), asked with
+ * anything, NaN too. At the positions before L values are finite, as in
+ * sparge_window_fwd; an e4m3 row that is NaN as a whole (byte 255) makes O NaN
+ * for the rows that see it, and lse too if it is K's, and touches no others.
+ * Workspace: sparge_cache_attn_workspace_bytes(...), asked with
  * the tensors' device current (0 if nothing is to be done or an argument is invalid). */
 size_t sparge_cache_attn_workspace_bytes(const sparge_cache* cache, const sparge_cache_batch* batch, int32_t H,
                                          int32_t max_new, int32_t max_len, const sparge_window* window);

@@ -230,3 +230,53 @@ def test_bytes_that_the_writer_does_not_store(sparge, byte, new):
         Q = (normal(17, new, 4, d) * 2.0 ** (max(-120, min(120, 127 - byte)) if which == 0 else 0)).to(torch.bfloat16)
         O, lse = attend(sparge, Q, (*codes, table), both, n)
         compare(O, lse, Q, *kv)
+
+
+@pytest.mark.parametrize("new", [1, 4, 20, 90])
+@pytest.mark.parametrize("where", ["v", "k"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_nan_reach_only_those_who_see_them(sparge, d, where, new):
+    """Rows with an infinity among the new tokens and just outside a window: O is NaN for the rows that see one, in V or
+    K, and as if it were not there for the others of its tile; V does not reach the log-sum-exp."""
+    n = 700
+    k, v, Q = normal(23, n, d), normal(24, n, d), normal(25, new, 4, d).to(torch.bfloat16)
+    first = n - new
+    bad = [first - 41, 5] + ([first + new // 2] if new > 1 else [])
+    x = v if where == "v" else k
+    x[bad, 7] = math.inf
+    clean = k.clone(), v.clone()
+    clean[0 if where == "k" else 1][bad] = 0
+    cache, exp, _ = cache_of(sparge, k, v, 16)
+    at = torch.arange(n, device="cuda")
+    for win in ((40, 0, 0, 1), (40, 0, 10, 1), (-1, 0, 0, 1)):
+        O, lse = attend(sparge, Q, cache, exp, n, win)
+        seen = visible(at[-new:], at, n, *win)
+        hit = seen[:, bad].any(1)
+        k64, v64 = (e4m3_rows(t.to(torch.bfloat16))[0] for t in clean)
+        for h in range(4):
+            assert torch.isnan(O[hit, h]).all()
+            o, ls, to, _, tl = rows_fwd(Q[:, h], k64, v64, seen)
+            close(O[~hit, h], o[~hit], to[~hit], f"O, window {win}")
+            keep = ~hit if where == "k" else torch.ones_like(hit)
+            close(lse[keep, h], ls[keep], tl[keep], f"lse, window {win}")
+            assert torch.isnan(lse[~keep, h]).all()
+
+
+def test_nan_rows_in_a_long_split_cache(sparge):
+    """The same where many CTAs share an item: the partial that holds the row makes O NaN, the log-sum-exp stays."""
+    n, d = 40000, 128
+    k, v = normal(26, n, d), normal(27, n, d)
+    v[31000, 0] = -math.inf
+    clean = v.clone()
+    clean[31000] = 0
+    cache, exp, (k64, _) = cache_of(sparge, k, v)
+    v64 = e4m3_rows(clean.to(torch.bfloat16))[0]
+    for new in (1, 20, 200):
+        Q = normal(28, new, 4, d).to(torch.bfloat16)
+        O, lse = attend(sparge, Q, cache, exp, n)
+        assert torch.isnan(O).all()
+        at = torch.arange(n, device="cuda")
+        seen = visible(at[-new:], at, n, -1, 0, 0, 1)
+        for h in range(4):
+            _, ls, _, _, tl = rows_fwd(Q[:, h], k64, v64, seen)
+            close(lse[:, h], ls, tl, "lse")
