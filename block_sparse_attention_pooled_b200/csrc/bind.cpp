@@ -133,13 +133,16 @@ WindowArgs window_args(const Tensor& Q, const Tensor& K, const Tensor& V, int le
 }
 
 Tensor window_fwd(const Tensor& Q, const Tensor& K, const Tensor& V, int left, int right, int sinks, int unit,
-                  const MaybeTensor& lens, const MaybeTensor& O, const MaybeTensor& lse, const StreamArg& stream) {
+                  const MaybeTensor& lens, const MaybeTensor& O, const MaybeTensor& lse, const MaybeTensor& workspace,
+                  const StreamArg& stream) {
   const WindowArgs a = window_args(Q, K, V, left, right, sinks, unit, lens);
   Launch on(Q.device(), stream);
-  Tensor out = on.out(O, "O", at::kBFloat16, Q.sizes());
+  Tensor out = on.out(O, "O", at::kBFloat16, Q.sizes()), keep;
   float* l = lse ? static_cast<float*>(want(*lse, "lse", at::kFloat, Q.sizes().slice(0, 3), Q.device())) : nullptr;
+  auto ws = on.space(
+      workspace, [&] { return sparge_window_workspace_bytes(SPARGE_OP_WINDOW_FWD, &a.shape, &a.window); }, keep);
   check(sparge_window_fwd(Q.data_ptr(), K.data_ptr(), V.data_ptr(), &a.shape, &a.window, a.lens, out.data_ptr(), l,
-                          nullptr, 0, on.stream()),
+                          ws.first, ws.second, on.stream()),
         "sparge_window_fwd");
   return out;
 }

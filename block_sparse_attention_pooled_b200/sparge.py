@@ -349,8 +349,8 @@ def sparge_window_fwd(Q, K, V, left: int, right: int, sinks: int = 0, unit: int 
                       workspace=None, stream=None):
     """Attention with a sliding window and sinks over [B,H,N,d] (K, V: [B,Hkv,N,d]); left and right count units of
     `unit` tokens, -1 for no limit; lens: int32 [B] lengths of a padded batch. Returns O (and fills lse if given).
-    It needs no workspace."""
-    return _bind.window_fwd(Q, K, V, left, right, sinks, unit, lens, O, lse, _on(stream))
+    It needs no workspace now; one that is given is checked as elsewhere."""
+    return _bind.window_fwd(Q, K, V, left, right, sinks, unit, lens, O, lse, workspace, _on(stream))
 
 
 def sparge_window_bwd(Q, K, V, O, lse, dO, left: int, right: int, sinks: int = 0, unit: int = 1, lens=None, dQ=None,

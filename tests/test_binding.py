@@ -187,3 +187,16 @@ def test_outputs_for_another_stream(lib):
         torch.empty_like(want).fill_(9)
     torch.cuda.synchronize()
     assert torch.equal(copy, want)
+
+
+@pytest.mark.gpu
+def test_forward_workspace_is_checked(lib):
+    """The windowed forward looks at a workspace as the other calls do."""
+    Q, K, V = window_inputs()
+    want = lib.sparge_window_fwd(Q, K, V, 5, 0)
+    assert torch.equal(lib.sparge_window_fwd(Q, K, V, 5, 0, workspace=torch.empty(256, dtype=torch.uint8, device="cuda")), want)
+    for bad in (torch.empty(256, dtype=torch.uint8), torch.empty(256, 2, dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(ValueError):
+            lib.sparge_window_fwd(Q, K, V, 5, 0, workspace=bad)
+    with pytest.raises(TypeError):
+        lib.sparge_window_fwd(Q, K, V, 5, 0, workspace=256)
