@@ -1,7 +1,8 @@
 // Attention of few new tokens over the paged cache (one token of each of G
 // heads when decoding): bound by reading the cache once.
 //
-// Persistent CTAs with equal runs of 64-key tiles (cache_sched.cuh). Two producer
+// Persistent CTAs with equal runs of key tiles (cache_sched.cuh; 64 keys of bf16,
+// 128 of e4m3). Two producer
 // warps fill a ring of K and V tiles by TMA through the page table (one box per
 // page and 64 columns; 128 bytes of swizzle); the other warps take whole tiles
 // in turn, each with a running maximum and sum and an accumulator of its own,

@@ -1,16 +1,17 @@
 // Windowed attention forward on the 5th-generation tensor cores, over whole
-// sequences and over the paged cache.
+// sequences (cache_chunk.cuh has the same over the paged cache).
 //
 //   O_i = sum_j softmax_j(q_i . k_j / sqrt(d)) v_j over the keys visible to i,
 // in one pass over the keys with a running maximum and sum per row.
 //
-// One CTA per SM takes work items of 256 rows (two 128-row tiles A and B) of
-// one K/V head and walks the 128-key tiles that any of its rows may see: the
-// sinks below the window, then the window. Roles:
+// A CTA per work item of 256 rows (two 128-row tiles A and B) of one head; the
+// one on each SM goes on with the items of CTAs that have not started. It walks
+// the 128-key tiles that any of the rows may see: the sinks below the window,
+// then the window. Roles:
 //   warp 0       producer: Q, then K and V tiles into a ring, by TMA; a tile
-//                that reaches past the sequence's end (or into a page that is
-//                not there) gets zeros in the rows that do not exist, so that
-//                what memory holds there never meets a probability of 0;
+//                that reaches past the sequence's end gets zeros in the rows
+//                that do not exist, so that what memory holds there never meets
+//                a probability of 0;
 //   warp 1       MMA issuer and TMEM owner;
 //   warps 4..7   softmax of tile A: one row (TMEM lane) per thread;
 //   warps 8..11  softmax of tile B.

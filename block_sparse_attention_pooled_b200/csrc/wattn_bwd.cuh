@@ -5,8 +5,9 @@
 //
 // Two kernels recompute the scores, one per direction of the sums, so that
 // each sum stays in TMEM and no atomics are needed: 7 products of 128 x 128 x d
-// per tile pair instead of 5 (bwd_dot_kernel gives D_i first).
-//   window_dq_kernel    one CTA per 128 query rows, over their key tiles;
+// per tile pair instead of 5.
+//   window_dq_kernel    one CTA per 128 query rows, over their key tiles; forms D_i
+//                       and leaves it for the other;
 //   window_dkdv_kernel  one CTA per 128 keys (and part of the query tiles),
 //                       over the query tiles of all heads that share them.
 // Both: 128 x 128 score tiles (a 64-wide tile would be bound by the reads of
@@ -188,8 +189,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
   // size of dS where a row sees few keys. So with few key tiles they are gone
   // through twice, first for D_i = sum_j P_ij dP_ij in fp32. Relative error of dQ
   // over 8 x 4000 rows (the roundings of dS and dQ alone: 2.35e-3): 2 keys 4.1e-3
-  // -> 2.4e-3, 512 keys 2.53e-3 -> 2.44e-3, for 2 of 55 and 8 of 80 us a step;
-  // from nine tiles on it is below 2.5e-3 without.
+  // -> 2.4e-3, 512 keys 2.53e-3 -> 2.44e-3; from nine tiles on it is below 2.5e-3
+  // without. A step of 2 x 8 heads x 2047 tokens that see 511 keys: 62 -> 67 us.
   const bool twice = T <= 8;
   const int U = twice ? 2 * T : T;
   auto key_of = [&](int u) { return kt.key0(u < T ? u : u - T); };

@@ -375,6 +375,7 @@ def sparge_cache_attn(Q, k_pages, v_pages, page_table, first, cu_new, max_new: i
                       workspace=None, stream=None):
     """Attention of the new tokens Q (bf16 [T,H,d], any token stride), which stand at positions first[b], ... of their
     sequences, over the paged cache that holds those positions already. max_new and max_len bound a sequence's new
-    tokens and its length. Returns O [T,H,d] (and fills lse [T,H] if given)."""
+    tokens, by which the work is split, and its length, which has to be at least 1 and decides nothing. Returns O
+    [T,H,d] (and fills lse [T,H] if given)."""
     return _bind.cache_attn(Q, k_pages, v_pages, page_table, first, cu_new, max_new, max_len, left, right, sinks, unit,
                             k_exp, v_exp, O, lse, workspace, _on(stream))

@@ -337,8 +337,11 @@ sparge_status sparge_window_fwd(const void* Q, const void* K, const void* V, con
  *   dO          bf16 [B,H,N,d];  dQ: bf16 [B,H,N,d];  dK, dV: bf16 [B,Hkv,N,d].
  * Rows at or past L get zeros in dQ, dK and dV; what dO holds there does not
  * matter. A row that sees a single key has dS = 0 exactly. Precision: fp32
- * scores, P and dS rounded to bf16 for their products, fp32 sums, D_i from the
- * bf16 O. No atomics: identical inputs give identical
+ * scores, P and dS rounded to bf16 for their products, fp32 sums. D_i: where the
+ * keys of a row's 128-row tile lie in at most eight 128-key tiles it is
+ * sum_j P_ij (dO_i . v_j) in fp32 (the same number; O is not read), elsewhere
+ * dO_i . O_i from the bf16 O; dK takes it corrected by the sum of dS over the
+ * keys, which is 0 but for its error. No atomics: identical inputs give identical
  * gradients. Workspace: sparge_window_workspace_bytes(SPARGE_OP_WINDOW_BWD, ...). */
 sparge_status sparge_window_bwd(const void* Q, const void* K, const void* V, const sparge_window_shape* shape,
                                 const sparge_window* window, const int32_t* lens, const void* O, const float* lse,
@@ -400,8 +403,10 @@ sparge_status sparge_cache_read(const sparge_cache* cache, const sparge_cache_ba
  *   Q           bf16 [tokens, H, d], token t's row at Q + t * q_stride (elements,
  *               a multiple of 8), heads contiguous.
  *   H           query heads, a multiple of cache->Hkv, at most 128 times it.
- *   max_new, max_len  bounds of a sequence's new tokens and of L, >= 1. They
- *               choose how the work is split, not what is computed.
+ *   max_new     bound of a sequence's new tokens, >= 1. It chooses the kernel
+ *               and how the work is split, not what is computed.
+ *   max_len     bound of L, >= 1. Kept for the callers that pass it: the
+ *               kernels read the lengths on the device, so it chooses nothing.
  *   O           bf16 [tokens, H, d], contiguous;  lse: optional float [tokens, H].
  * Precision, and the magnitudes of scores and V that 32 bits hold: bf16 as
  * sparge_window_fwd. e4m3: the same magnitudes; the codes enter the products
