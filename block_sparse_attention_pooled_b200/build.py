@@ -2,6 +2,7 @@
 entry points, _bind, against it and torch."""
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -17,6 +18,7 @@ HEADERS = [os.path.join(PKG, "csrc", f) for f in ("ptx.cuh", "mask.cuh", "attn.c
 LIB = os.path.join(PKG, "libsparge.so")
 BIND_SRC = os.path.join(PKG, "csrc", "bind.cpp")
 BIND = os.path.join(PKG, "_bind" + sysconfig.get_config_var("EXT_SUFFIX"))
+BIND_FOR = os.path.join(PKG, "_build", "bind_for.txt")  # the torch and Python that _bind was built for
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -47,10 +49,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
             cmd.insert(1, "-Xptxas=-v")
         subprocess.check_call(cmd, stdout=None if verbose else subprocess.DEVNULL)
         os.replace(tmp, LIB)
-    deps = [BIND_SRC, os.path.join(ROOT, "include", "sparge.h")]
-    if force or not os.path.exists(BIND) or any(os.path.getmtime(f) > os.path.getmtime(BIND) for f in deps):
+    if force or _bind_stale():
         _build_bind()
+        os.makedirs(os.path.dirname(BIND_FOR), exist_ok=True)
+        with open(BIND_FOR, "w") as f:
+            f.write(_bind_target())
     return LIB
+
+
+def _bind_target() -> str:
+    """What the binding has to be built for; its name holds no more than the Python version."""
+    return f"torch {importlib.metadata.version('torch')}, Python {sys.version.split()[0]}"
+
+
+def _bind_stale() -> bool:
+    if not (os.path.exists(BIND) and os.path.exists(BIND_FOR)):
+        return True
+    with open(BIND_FOR) as f:
+        if f.read() != _bind_target():
+            return True
+    deps = [BIND_SRC, os.path.join(ROOT, "include", "sparge.h")]
+    return any(os.path.getmtime(f) > os.path.getmtime(BIND) for f in deps)
 
 
 def _build_bind() -> None:

@@ -200,3 +200,23 @@ def test_forward_workspace_is_checked(lib):
             lib.sparge_window_fwd(Q, K, V, 5, 0, workspace=bad)
     with pytest.raises(TypeError):
         lib.sparge_window_fwd(Q, K, V, 5, 0, workspace=256)
+
+
+def test_binding_is_rebuilt_for_another_torch(lib, monkeypatch, tmp_path):
+    """Up to date: left alone. Built for another torch, or not known for which: built anew, and noted."""
+    from block_sparse_attention_pooled_b200 import build
+
+    built, note = [], tmp_path / "sub" / "bind_for.txt"
+    monkeypatch.setattr(build, "_build_bind", lambda: built.append(1))
+    build.build()
+    assert built == []
+    monkeypatch.setattr(build, "BIND_FOR", str(note))
+    build.build()
+    assert built == [1]
+    build.build()
+    assert built == [1]
+    note.write_text("torch 2.10.0, Python 3.12.3")
+    build.build()
+    assert built == [1, 1]
+    build.build()
+    assert built == [1, 1]
