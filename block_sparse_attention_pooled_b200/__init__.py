@@ -2,7 +2,8 @@
 sparse + linear mix, as CUDA kernels for sm_100a behind a C ABI.
 
 The CUDA entry points live in :mod:`block_sparse_attention_pooled_b200.sparge`
-(importing it loads ``libsparge.so`` and ``_bind`` and fails loudly when one of them is missing).
+(importing it loads ``libsparge.so`` and fails loudly when it is missing; calls of windowed and cached attention fail
+loudly when ``_bind`` is).
 :mod:`block_sparse_attention_pooled_b200.synth` generates seeded inputs.
 """
 

@@ -1,8 +1,9 @@
 """Python binding of the C ABI in include/sparge.h (argument marshalling only).
 
-Importing this module loads ``libsparge.so`` and the compiled binding ``_bind``
-from the package directory and raises ImportError when one of them is missing:
-there is no fallback implementation.
+Importing this module loads ``libsparge.so`` from the package directory and
+raises ImportError when it is missing. Windowed and cached attention are bound
+by the compiled ``_bind`` there; without it their calls raise ImportError. There
+is no fallback implementation.
 Tensors are torch CUDA tensors; every call is enqueued on the current torch
 stream (or the stream given) and returns without synchronising.
 """
@@ -19,11 +20,23 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsparge.
 if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{_LIB_PATH} is missing: build it with `python -m block_sparse_attention_pooled_b200.build`")
 _lib = ctypes.CDLL(_LIB_PATH)
+
+
+class _NoBind:
+    """In place of the compiled binding where it cannot be loaded: its calls say so, the other entry points do without."""
+
+    def __init__(self, why: ImportError):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"_bind is missing or was built for another torch: rebuild it with "
+                          f"`python -m block_sparse_attention_pooled_b200.build --force` ({self._why})") from self._why
+
+
 try:
     from . import _bind
 except ImportError as e:
-    raise ImportError(f"_bind is missing or was built for another torch: rebuild it with "
-                      f"`python -m block_sparse_attention_pooled_b200.build --force` ({e})") from e
+    _bind = _NoBind(e)
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_TIMEOUT = range(6)
 OP_MASK, OP_ATTN, OP_SLA2, OP_ATTN_Q8, OP_MASK_ROUTER, OP_ATTN_BWD, OP_SLA2_BWD = 0, 1, 2, 3, 4, 5, 6
@@ -338,7 +351,8 @@ def device_status(stream=None) -> int:
 # microseconds on the GPU, so the arguments are checked in compiled code
 # (csrc/bind.cpp); what is here are the names, the defaults and what they do.
 # ---------------------------------------------------------------------------
-_bind.set_error(SpargeError)
+if not isinstance(_bind, _NoBind):
+    _bind.set_error(SpargeError)
 
 
 def _on(stream):

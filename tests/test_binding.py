@@ -220,3 +220,31 @@ def test_binding_is_rebuilt_for_another_torch(lib, monkeypatch, tmp_path):
     assert built == [1, 1]
     build.build()
     assert built == [1, 1]
+
+
+def test_without_the_compiled_binding(lib):
+    """The entry points that it does not serve work without it; the others say what is missing when they are called."""
+    import subprocess
+    import sys
+
+    code = """
+import sys
+sys.modules["block_sparse_attention_pooled_b200._bind"] = None  # its import raises ImportError
+from block_sparse_attention_pooled_b200 import sparge
+assert sparge.workspace_bytes(sparge.OP_ATTN_BWD, sparge.Shape(1, 2, 1000, 128, 128, 64)) > 0
+for name, args in (("sparge_window_fwd", (1, 1, 1, 0, 0)), ("sparge_window_bwd", (1,) * 6 + (0, 0)),
+                   ("sparge_cache_write", (1,) * 7), ("sparge_cache_read", (1,) * 6), ("sparge_cache_attn", (1,) * 8)):
+    try:
+        getattr(sparge, name)(*args)
+    except ImportError as e:
+        assert "_bind" in str(e) and "build" in str(e), e
+    else:
+        raise AssertionError(name)
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=build_root())
+
+
+def build_root():
+    from block_sparse_attention_pooled_b200 import build
+
+    return build.ROOT
