@@ -59,6 +59,13 @@ cudaError_t launch_next(void (*kernel)(Params...), unsigned grid, unsigned threa
 // one CTA works through its rows in order, so long runs are cut into pieces of
 // at most about a third of an SM's share of the whole work, or about its share
 // where that is small (a piece's fp32 sums are written and read once more).
+// Whole backward, us, with pieces of a sixth / a third / the whole share: 480p
+// clip of frames 3180 / 3100 / 3099 (half the time is this kernel's), 12 heads x
+// 8000 tokens that see 1024: 376 / 291 / 269, 8 x 4096 causal: 196 / 165 / 117.
+// The third is not the best where runs are long. With little work, pieces of at
+// least 2 / 8 tiles: 4 heads x 1000 tokens of d 64 29 / 35, 2 x 8 x 2047 76 / 78.
+// (148: the SMs of the one GPU this is built for, so that the workspace does not
+// depend on the current device.)
 struct KvSplit {
   int tiles, sink_tiles, sink_pieces, pieces;
   size_t slots;  // of [2][128][d] fp32
@@ -228,7 +235,10 @@ struct AttnPlan {
 };
 
 // Up to 16 rows a sequence the time is the cache's bytes and mma.sync keeps up
-// with them; more rows go to tcgen05, whose tiles have 128.
+// with them; more rows go to tcgen05, whose tiles have 128. 24 sequences of
+// 16 k keys and 4 K/V heads, 16 rows, us by mma.sync / by tcgen05: d 128 bf16
+// 130 / 169, e4m3 160 / 197; d 64 92 / 136 and 90 / 150; two such sequences
+// 29 / 37 and 37 / 38. 20 rows take 157 (bf16) and 198 (e4m3) by tcgen05.
 AttnPlan attn_plan(const sparge_cache* c, const sparge_cache_batch* b, int32_t H, int32_t max_new) {
   AttnPlan a;
   const int64_t G = H / c->Hkv, rows = G * std::min(max_new, b->tokens);
@@ -239,6 +249,10 @@ AttnPlan attn_plan(const sparge_cache* c, const sparge_cache_batch* b, int32_t H
   // many, a whole number of CTAs per row tile keeps them at the same keys at the
   // same time, so that L2 serves all but the first (1560 rows over 32760 cached
   // tokens of 12 heads, 7 row tiles: 147 CTAs read 0.2 GB from memory, 148 1.3 GB).
+  // It pays where few CTAs stand aside for it. Aligned from 15/16 of the CTAs on /
+  // never / from 7/8 on, us over bf16: that frame 292 / 332 / 292, 4000 rows x 8
+  // heads over 24 k 328 / 389 / 349, 2 x 700 tokens over 20 k 243 / 240 / 257,
+  // 5 x 640 over 9 k 150 / 146 / 138.
   if (a.rows > 16 && (int64_t)b->B * max_new == b->tokens) {
     const int64_t tiles = (int64_t)b->B * ceil_div(max_new, a.tpt);
     const int64_t even = tiles > 0 ? a.ctas / tiles * tiles : 0;

@@ -335,6 +335,7 @@ sparge_status sparge_window_fwd(const void* Q, const void* K, const void* V, con
  *   dV_j = sum_i P_ij dO_i, the sums over i also over the heads that share K, V.
  *   O, lse      the forward's, for the same inputs.
  *   dO          bf16 [B,H,N,d];  dQ: bf16 [B,H,N,d];  dK, dV: bf16 [B,Hkv,N,d].
+ * Values at positions before L, dO among them, have to be finite.
  * Rows at or past L get zeros in dQ, dK and dV; what dO holds there does not
  * matter. A row that sees a single key has dS = 0 exactly. Precision: fp32
  * scores, P and dS rounded to bf16 for their products, fp32 sums. D_i: where the
@@ -372,7 +373,8 @@ typedef struct {
  * cu[b] .. cu[b+1] - 1 of the token tensors and stand at the positions
  * first[b], first[b] + 1, ... of its cache.
  *   page_table  int32 [B, max_pages];  first: int32 [B], >= 0;
- *   cu          int32 [B + 1], ascending from 0. All device memory.
+ *   cu          int32 [B + 1], ascending from 0. All device memory. No position
+ *               reaches 2^30.
  * tokens is the token tensors' number of rows; rows at or past cu[B] are
  * neither read nor written. */
 typedef struct {
