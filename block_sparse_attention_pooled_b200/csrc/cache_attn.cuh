@@ -446,6 +446,9 @@ __global__ void __launch_bounds__(DecSmem<D, E4M3, R8>::kThreads)
         if (__any_sync(0xffffffffu, top[0] > m_run[x][0] || top[1] > m_run[x][1])) {
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
+            // x_j + e_j is rounded: the reference lies a step above it, so that P
+            // stays in fp16's range where a step is more than its last binade.
+            if (E4M3 && top[y] > m_run[x][y]) top[y] = fmaf(fabsf(top[y]), 0x1p-23f, top[y]);
             const float f = top[y] == -INFINITY ? 1.0f : ex2_approx(m_run[x][y] - top[y]);
             if (!E4M3) l_run[x][y] *= f;
             m_run[x][y] = top[y];

@@ -319,7 +319,7 @@ size_t sparge_window_workspace_bytes(int op, const sparge_window_shape* shape, c
  *   lse         optional output, float [B,H,N], natural logarithm.
  * Values at positions before L have to be finite: a key that one row of a
  * tile sees and another does not reaches the latter as 0 * v. Scores and sums
- * are in 32 bits: q . k / sqrt(d) has to stay below 2^29 in magnitude, and V's
+ * are in 32 bits: q . k / sqrt(d) has to stay below 2^25 in magnitude, and V's
  * magnitude times the number of keys that a row sees below 2^119 (the sum is
  * divided at the end).
  * Limits: d 64 or 128, B * Hkv <= 65535. Workspace:
@@ -338,7 +338,8 @@ sparge_status sparge_window_fwd(const void* Q, const void* K, const void* V, con
  * Values at positions before L, dO among them, have to be finite.
  * Rows at or past L get zeros in dQ, dK and dV; what dO holds there does not
  * matter. A row that sees a single key has dS = 0 exactly. Precision: fp32
- * scores, P and dS rounded to bf16 for their products, fp32 sums. D_i: where the
+ * scores and lse (P is off by up to 2^-22 |lse| of itself, which passes its
+ * rounding to bf16 from |lse| = 2^14 on), P and dS rounded to bf16 for their products, fp32 sums. D_i: where the
  * keys of a row's 128-row tile lie in at most eight 128-key tiles it is
  * sum_j P_ij (dO_i . v_j) in fp32 (the same number; O is not read), elsewhere
  * dO_i . O_i from the bf16 O; dK takes it corrected by the sum of dS over the

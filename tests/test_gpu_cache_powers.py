@@ -280,3 +280,19 @@ def test_nan_rows_in_a_long_split_cache(sparge):
         for h in range(4):
             _, ls, _, _, tl = rows_fwd(Q[:, h], k64, v64, seen)
             close(lse[:, h], ls, tl, "lse")
+
+
+@pytest.mark.parametrize("new", [1, 4, 20])
+@pytest.mark.parametrize("power", [3, 12, 20, 22, 23, 24])
+def test_equal_large_scores_of_rows_of_different_powers(sparge, power, new):
+    """Scores of 2^power for some keys (exact in 32 bits), of the opposite sign for the others, and V's powers from row to
+    row: sums of score and power are rounded, the mean over the best keys stays."""
+    n, d = 600, 64
+    for seed in range(4):
+        k, v = torch.zeros(n, d, device="cuda"), normal(30 + seed, n, d)
+        v *= torch.exp2(torch.randint(-9, 10, (n, 1), generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda"))
+        k[:, 0] = -8.0
+        k[::37, 0] = 8.0
+        Q = torch.zeros(new, 4, d, device="cuda")
+        Q[..., 0] = 2.0 ** power * torch.tensor([1.0, 1.25, 1.5, 1.75], device="cuda")
+        check(sparge, k, v, Q.to(torch.bfloat16))
